@@ -22,6 +22,9 @@ paragraph on the 16-bit branch, names the two fusions):
     y = w4a4_gemm_lora_up(codes, scales, w_codes, w_scales, lora_act, lora_up, bias)
 
 and the offline host packer (``smooth_from_absmax``, ``pack_weights``).
+
+The operators around these linears in a transformer block (the 8-bit linear,
+the gated residual norms, rotary positions with several axes) are in block.py.
 """
 from __future__ import annotations
 
@@ -37,9 +40,25 @@ __all__ = ["SvdqError", "lib", "check_device", "quantize_act_lora_down", "w4a4_g
            "EPILOGUES", "smooth_from_absmax", "pack_weights", "awq_w4a16_gemm", "awq_w4a16_gemm_stacked",
            "awq_pack_weights",
            "quantize_act_lora_down_fp4", "fp4_gemm_lora_up", "pack_weights_fp4",
-           "release_workspaces", "GROUP_SIZE"]
+           "release_workspaces", "GROUP_SIZE",
+           "quantize_act_int8", "w8a8_gemm", "pack_weights_int8", "gate_norm_modulate", "rope_axes",
+           "rope_axes_tables"]
 
 GROUP_SIZE = 64
+
+# the block operators live in block.py, which needs torch; it is imported when
+# one of them is first used
+_BLOCK = ("quantize_act_int8", "w8a8_gemm", "pack_weights_int8", "gate_norm_modulate", "rope_axes",
+          "rope_axes_tables")
+
+
+def __getattr__(name):
+    if name in _BLOCK:
+        from . import block
+        for n in _BLOCK:
+            globals()[n] = getattr(block, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _torch():

@@ -61,6 +61,25 @@ SIGNATURES = {
     "svdq_awq_w4a16_gemm_stacked": (ctypes.c_int, [
         _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _i64, _i64,
         _c_void_p, _c_void_p]),
+    "svdq_quantize_act_int8": (ctypes.c_int, [
+        _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _c_void_p]),
+    "svdq_w8a8_gemm": (ctypes.c_int, [
+        _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, ctypes.c_int,
+        _c_void_p, _c_void_p, _size, _c_void_p]),
+    "svdq_w8a8_gemm_workspace_size": (_size, [_i64, _i64, _i64]),
+    "svdq_gate_norm_modulate": (ctypes.c_int, [
+        _c_void_p, ctypes.c_int, _i64, _c_void_p, _i64, ctypes.c_int, _c_void_p, _c_void_p, _i64, _i64,
+        ctypes.c_float, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, ctypes.c_float, _i64, _i64,
+        _c_void_p, _i64, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "svdq_rope_axes_tables": (ctypes.c_int, [
+        _c_void_p, ctypes.c_int, _i64, _i64, _c_void_p, ctypes.c_double, ctypes.c_int, _c_void_p, _c_void_p,
+        _c_void_p]),
+    "svdq_rope_axes": (ctypes.c_int, [
+        _c_void_p, _i64, _i64, _c_void_p, _i64, _i64, _i64, _i64, _c_void_p, ctypes.c_int, _i64, _i64,
+        _c_void_p, ctypes.c_double, ctypes.c_int, ctypes.c_int, _c_void_p, _c_void_p, ctypes.c_float,
+        _c_void_p, _i64, _c_void_p, _i64, _c_void_p]),
+    "svdq_pack_weights_int8": (ctypes.c_int, [
+        _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p]),
     "svdq_w4a4_group_acc_debug": (ctypes.c_int, [
         _c_void_p, _c_void_p, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p]),
     "svdq_smooth_from_absmax": (ctypes.c_int, [_c_void_p, _c_void_p, _i64, _i64, _c_void_p]),

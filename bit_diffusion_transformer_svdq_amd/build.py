@@ -34,7 +34,8 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HOST_API_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-D__HIP_PLATFORM_AMD__",
                   "-I", os.path.join(ROCM, "include")]
 KERNELS = ["quant_lora_down.hip", "w4a4_gemm_lora_up.hip", "w4a4_gemm_skinny.hip", "fp4_gemm_big.hip",
-           "awq_w4a16_gemm.hip"]
+           "awq_w4a16_gemm.hip", "w8a8_gemm.hip", "w8a8_skinny.hip", "gate_norm.hip", "rope_axes.hip"]
+HOST_API = ["api.cpp", "block_api.cpp"]
 
 
 def _hipcc() -> str:
@@ -68,10 +69,11 @@ def build(verbose: bool = False, save_temps: bool = False) -> str:
         _run(cmd, verbose)
         objs.append(obj)
     # the C ABI is host code: g++ against the HIP runtime API
-    api_obj = os.path.join(BUILD_DIR, "api.o")
-    _run(["g++", "-c", *HOST_API_FLAGS, "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, "api.cpp"),
-          "-o", api_obj], verbose)
-    objs.append(api_obj)
+    for src in HOST_API:
+        api_obj = os.path.join(BUILD_DIR, src.replace(".cpp", ".o"))
+        _run(["g++", "-c", *HOST_API_FLAGS, "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, src),
+              "-o", api_obj], verbose)
+        objs.append(api_obj)
     packer_obj = os.path.join(BUILD_DIR, "packer.o")
     _run(["g++", "-c", "-O3", "-march=x86-64-v3", "-std=c++17", "-fPIC", "-Wall", "-fno-fast-math",
           "-ffp-contract=off", "-I", INCLUDE, os.path.join(CSRC, "packer.cpp"), "-o", packer_obj], verbose)

@@ -12,34 +12,20 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cstdarg>
 #include <cstddef>
-#include <initializer_list>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 
 #include "svdq.h"
+#include "api_checks.h"
 #include "svdq_internal.h"
 
 namespace {
 
+using namespace svdq_api;
+
 thread_local char g_err[512] = {0};
-
-svdq_status fail(svdq_status s, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof(g_err), fmt, ap);
-  va_end(ap);
-  return s;
-}
-
-svdq_status ok() {
-  g_err[0] = 0;
-  return SVDQ_STATUS_SUCCESS;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr int kMaxDevices = 64;
 // 0 = unknown, otherwise 1 + svdq_status
@@ -63,57 +49,7 @@ svdq_status check_device_uncached(int device) {
   return ok();
 }
 
-svdq_status check_current_device() {
-  int dev = 0;
-  int count = 0;
-  hipError_t e = hipGetDeviceCount(&count);
-  if (e != hipSuccess || count <= 0) {
-    (void)hipGetLastError();
-    return fail(SVDQ_STATUS_NO_DEVICE, "no HIP device visible");
-  }
-  e = hipGetDevice(&dev);
-  if (e != hipSuccess) return fail(SVDQ_STATUS_HIP_ERROR, "hipGetDevice: %s", hipGetErrorString(e));
-  return svdq_check_device(dev);
-}
-
 bool rank_supported(int64_t r) { return r >= 0 && r <= 128 && r % 16 == 0; }
-
-// A device byte range an entry point reads or writes.  Inputs may share memory
-// with each other; an output may share memory with nothing else the call
-// touches (the kernels read inputs while other workgroups already write).
-struct Span {
-  const void* p;
-  size_t n;
-  const char* name;
-};
-
-bool overlap(const Span& a, const Span& b) {
-  if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + b.n && b0 < a0 + a.n;
-}
-
-svdq_status check_disjoint(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
-  for (auto o = outs.begin(); o != outs.end(); ++o) {
-    for (auto i = ins.begin(); i != ins.end(); ++i)
-      if (overlap(*o, *i)) return fail(SVDQ_STATUS_INVALID_VALUE, "output %s overlaps input %s", o->name, i->name);
-    for (auto o2 = o + 1; o2 != outs.end(); ++o2)
-      if (overlap(*o, *o2)) return fail(SVDQ_STATUS_INVALID_VALUE, "outputs %s and %s overlap", o->name, o2->name);
-  }
-  return SVDQ_STATUS_SUCCESS;
-}
-
-// A call that needs `need` bytes of workspace gets them from the caller.
-svdq_status check_workspace(const void* ws, size_t ws_bytes, size_t need, const char* query) {
-  if (need == 0) return SVDQ_STATUS_SUCCESS;
-  if (!ws) return fail(SVDQ_STATUS_INVALID_VALUE, "this shape needs a workspace of %zu bytes (%s)", need, query);
-  if (ws_bytes < need)
-    return fail(SVDQ_STATUS_INVALID_VALUE, "workspace of %zu bytes, this shape needs %zu (%s)", ws_bytes, need, query);
-  if (!aligned16(ws)) return fail(SVDQ_STATUS_INVALID_VALUE, "workspace must be 16-byte aligned");
-  return SVDQ_STATUS_SUCCESS;
-}
-
-size_t sz(int64_t a, int64_t b = 1, int64_t c = 1) { return (size_t)a * (size_t)b * (size_t)c; }
 
 }  // namespace
 
@@ -156,7 +92,7 @@ const char* svdq_status_string(svdq_status s) {
 
 const char* svdq_last_error(void) { return g_err; }
 
-int svdq_version(void) { return 200; }
+int svdq_version(void) { return 300; }
 
 svdq_status svdq_check_device(int device) {
   if (device < 0) return fail(SVDQ_STATUS_INVALID_VALUE, "negative device index %d", device);
@@ -554,6 +490,13 @@ svdq_status svdq_w4a4_group_acc_debug(const void* act_codes, const void* w_codes
 
 }  // extern "C"
 
-// host packer entry points live in packer.cpp; they use these helpers for errors
-svdq_status svdq_internal_fail(svdq_status s, const char* msg) { return fail(s, "%s", msg); }
-svdq_status svdq_internal_ok() { return ok(); }
+// entry points in other files (packer.cpp, block_api.cpp) and the checks of
+// api_checks.h set the thread's message through these
+svdq_status svdq_internal_fail(svdq_status s, const char* msg) {
+  snprintf(g_err, sizeof(g_err), "%s", msg);
+  return s;
+}
+svdq_status svdq_internal_ok() {
+  g_err[0] = 0;
+  return SVDQ_STATUS_SUCCESS;
+}

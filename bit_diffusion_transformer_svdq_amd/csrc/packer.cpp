@@ -18,6 +18,7 @@
 // order, so results do not depend on the thread count.
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
@@ -521,6 +522,69 @@ svdq_status svdq_awq_pack_weights(const uint16_t* w, const uint16_t* x_calib, in
   });
   std::memcpy(smooth, best.data(), sizeof(float) * static_cast<size_t>(K));
   if (alpha_out) *alpha_out = static_cast<float>(best_alpha);
+  return svdq_internal_ok();
+}
+
+}  // extern "C"
+
+namespace {
+
+// f(a, b) over [0, n) on several threads.  Where a thread cannot be started the
+// caller's thread does what is left, so nothing is thrown; f must not throw.
+template <class F>
+void parallel_rows(int64_t n, F f) {
+  const int T = static_cast<int>(std::min<int64_t>(thread_count(), n));
+  std::vector<std::thread> th;
+  int64_t done = 0;
+  try {
+    th.reserve(static_cast<size_t>(T));
+    for (int t = 0; t + 1 < T; ++t) {
+      const int64_t b = n * (t + 1) / T;
+      th.emplace_back(f, done, b);
+      done = b;
+    }
+  } catch (...) {
+  }
+  f(done, n);
+  for (auto& x : th) x.join();
+}
+
+}  // namespace
+
+extern "C" {
+
+svdq_status svdq_pack_weights_int8(const uint16_t* w, const float* smooth, int64_t N, int64_t K, int8_t* w_codes,
+                                   float* w_scales) {
+  if (!w || !w_codes || !w_scales) return svdq_internal_fail(SVDQ_STATUS_INVALID_VALUE, "null pointer");
+  if (N <= 0 || K <= 0) return svdq_internal_fail(SVDQ_STATUS_INVALID_VALUE, "N and K must be positive");
+  std::atomic<bool> finite{true};
+  parallel_rows(N, [&](int64_t a, int64_t b) {
+    for (int64_t n = a; n < b; ++n) {
+      const uint16_t* row = w + static_cast<size_t>(n) * K;
+      int8_t* q = w_codes + static_cast<size_t>(n) * K;
+      auto value = [&](int64_t k) {
+        return smooth ? bf16_to_double(row[k]) * static_cast<double>(smooth[k]) : bf16_to_double(row[k]);
+      };
+      double top = 0.0;
+      bool good = true;
+      for (int64_t k = 0; k < K; ++k) {
+        const double v = std::fabs(value(k));
+        good = good && std::isfinite(v);
+        top = std::max(top, v);
+      }
+      const float s = static_cast<float>(top / 127.0);
+      if (!good || !std::isfinite(s)) {
+        finite.store(false);
+        return;
+      }
+      w_scales[n] = s;
+      for (int64_t k = 0; k < K; ++k) {
+        const double t = s > 0.f ? std::nearbyint(value(k) / static_cast<double>(s)) : 0.0;
+        q[k] = static_cast<int8_t>(std::max(-127.0, std::min(127.0, t)));
+      }
+    }
+  });
+  if (!finite.load()) return svdq_internal_fail(SVDQ_STATUS_INVALID_VALUE, "a weight is not finite");
   return svdq_internal_ok();
 }
 

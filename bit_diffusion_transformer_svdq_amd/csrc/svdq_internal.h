@@ -151,6 +151,83 @@ hipError_t launch_awq_w4a16(const uint16_t* x, const float* smooth, const uint8_
                             const uint16_t* scales, const uint8_t* zeros, const uint16_t* bias,
                             int64_t L, int64_t M, int64_t N, int64_t K, uint16_t* y, hipStream_t stream);
 
+// The norms around a block (gate_norm.hip).  Shapes validated by the caller:
+// M > 0, C % 8 == 0, C <= kGateNormMaxC; strides in elements, multiples of 8.
+constexpr int kNormNone = 0;
+constexpr int kNormLayer = 1;
+constexpr int kNormRms = 2;
+constexpr int64_t kGateNormMaxC = 32768;
+struct GateNormArgs {
+  const void* x;                // residual stream [M, C], bf16 or fp32
+  const uint16_t* y;            // block output bf16 [M, C] or null
+  const uint16_t* post_weight;  // bf16 [C] or null
+  const uint16_t* gate;         // bf16 rows of C, or null
+  const uint16_t* weight;       // bf16 [C] or null
+  const uint16_t* scale;        // bf16 rows of C, or null
+  const uint16_t* shift;        // bf16 rows of C, or null
+  const float* smooth;          // fp32 [C] or null (8-bit output only)
+  void* h;                      // [M, C] of x's type (y given)
+  void* z;                      // bf16 [M, C], or int8 codes [M, C] (scales given)
+  float* scales;                // fp32 [M] or null
+  int64_t x_stride, y_stride, h_stride, gate_stride, mod_stride;
+  int M, C;
+  int gate_every, mod_every;    // rows that share a gate row, a scale / shift row
+  int post, norm, x_fp32;
+  float alpha, eps;
+};
+hipError_t launch_gate_norm(const GateNormArgs& a, hipStream_t stream);
+
+// Per-token 8-bit quantization.  M > 0, K % 64 == 0, K <= kInt8MaxK.
+constexpr int64_t kInt8MaxK = 65536;
+struct QuantInt8Args {
+  const uint16_t* x;    // bf16 [M, K]
+  const float* smooth;  // fp32 [K] or null
+  int8_t* codes;        // [M, K]
+  float* scales;        // [M]
+  int M, K;
+};
+hipError_t launch_quant_int8(const QuantInt8Args& a, hipStream_t stream);
+
+// The 8-bit linear (w8a8_gemm.hip): exact int32 sums, one fp32 scale per token
+// and per output channel.  M > 0, N % 64 == 0, K % 64 == 0, K <= kInt8MaxK.
+struct W8a8Args {
+  const int8_t* act;        // codes [M, K]
+  const float* act_scales;  // [M]
+  const int8_t* w;          // codes [N, K]
+  const float* w_scales;    // [N]
+  const uint16_t* bias;     // bf16 [N] or null
+  uint16_t* y;              // bf16 [M, N]
+  int M, N, K, epilogue;
+};
+size_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_w8a8_gemm(const W8a8Args& a, Workspace ws, hipStream_t stream);
+
+// Rotary positions with several axes (rope_axes.hip).
+constexpr int kRopeMaxAngles = 128;  // R / 2
+constexpr int kRopeMaxAxes = 8;
+struct RopeAxes {
+  int n;                     // axes
+  int width[kRopeMaxAxes];   // channels of each, even
+  int half;                  // R / 2, R = sum of the widths
+  bool shared;               // one spectrum over R instead of one per axis
+  double theta;
+};
+struct RopeArgs {
+  const uint16_t *q, *k;           // bf16, token m's heads at m * stride; k may be null (k_heads 0)
+  uint16_t *q_out, *k_out;
+  const uint16_t *q_norm, *k_norm; // bf16 [D], both or neither (k_norm null with k_heads 0)
+  const void* positions;           // fp32 or int32 [pos_rows, n_axes]; token m reads row m % pos_rows
+  int64_t q_stride, k_stride, qo_stride, ko_stride;
+  int64_t pos_rows;
+  int M, q_heads, k_heads, D;
+  int pos_int;
+  float eps;
+  int n_axes, half, lanes;         // set by the launcher
+};
+hipError_t launch_rope_tables(const void* positions, bool pos_int, const RopeAxes& axes, int64_t M, float* cos,
+                              float* sin, hipStream_t stream);
+hipError_t launch_rope_axes(const RopeArgs& args, const RopeAxes& axes, bool halves, hipStream_t stream);
+
 // Test hook: K-splits per tile of the tiled kernel (0 = choose by shape;
 // clipped to the number of group pairs; ignored for the QKV epilogue).
 void set_gemm_splits_override(int splits);

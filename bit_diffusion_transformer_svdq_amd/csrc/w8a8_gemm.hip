@@ -1,0 +1,405 @@
+// The 8-bit linear on gfx950: Y = (sum_k q_x q_w) s_x s_w + b with exact int32
+// sums, one fp32 scale per token and one per output channel, and an optional
+// GELU (tanh form) before the one bf16 rounding.  It serves the projections
+// that are kept out of the 4-bit path (mind-verse.de, "Effiziente Optimierung
+// von Diffusionsmodellen durch Nunchaku 4-Bit-Quantisierung", section "Nunchaku
+// Lite: Nahtlose Integration in Diffusers": precision-sensitive layers).
+//
+// With no dequantization inside the K loop the kernel is a plain int8 GEMM, and
+// what bounds it is the matrix core (2 M N K / 5 POP/s) next to the LDS: a k
+// stage of 128 bytes per row costs the LDS its DMA writes plus each operand row
+// once per wave that needs it, so the wave tile is as large as the registers
+// allow.
+//  * workgroup tile 64 WI weight rows x 64 WJ token rows, 4 waves as 2 x 2, each
+//    32 WI x 32 WJ = WI x WJ tiles of v_mfma_i32_32x32x32_i8 (WI = WJ = 4: 256
+//    int32 accumulators per lane, one wave per SIMD);
+//  * two LDS stages of 128 bytes per row, filled by global_load_lds_dwordx4 with
+//    8 whole 128-byte row runs per instruction.  A stage is computed in two
+//    halves: while the MFMAs of the first run, the fragments of the second are
+//    read; after that the stage's LDS is free, its DMA for stage q + 2 is
+//    issued, and while the second half's MFMAs run the first half of stage
+//    q + 1 is read.  One barrier per stage, with a whole stage of MFMAs between
+//    a DMA and the wait for it;
+//  * 16-byte granule g of row R sits at slot 8 R + (g ^ R[2:0]): the 8 rows of a
+//    fragment-read phase take all 32 banks;
+//  * few tiles: K is split over workgroups, whose int32 partials meet in the
+//    caller's workspace (integer sums: the order does not matter).
+//
+// The MFMA A operand is the weight tile (rows n), B the token tile (columns m),
+// so lane l holds Y[m = l % 32][n = 8 k + 4 (l / 32) + v] of each 32 x 32 tile; Y
+// leaves through LDS in runs of 64 WI bytes per row.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "row_device.h"
+#include "w8a8.h"
+
+namespace svdq {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
+typedef unsigned v4u __attribute__((ext_vector_type(4)));
+typedef unsigned int u32;
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) void glb_void;
+
+constexpr int kThreads = 256;  // 4 waves
+constexpr int kXcds = 8;
+constexpr int kBandM = 4;
+
+// wait until at most n vector-memory operations of this wave are outstanding
+// and all of its LDS operations are done
+template <int n>
+__device__ __forceinline__ void wait_vm_lds() {
+  static_assert(n >= 0 && n < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((n & 0xF) | (0x7 << 4) | ((n >> 4) << 14));
+}
+
+// workgroup barrier without the memory fences of __syncthreads (the waits it
+// needs are explicit); the empty asm keeps LDS accesses on their side
+__device__ __forceinline__ void barrier() {
+  __asm__ volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ void dma16(const void* gptr, uint8_t* lds_wave_base) {
+  __builtin_amdgcn_global_load_lds((glb_void*)gptr, (lds_void*)lds_wave_base, 16, 0, 0);
+}
+
+// Workgroup id -> (tile_m, tile_n).  Workgroups go round-robin over the 8
+// XCDs (id % 8), each with its own L2; the ids of one XCD take one contiguous
+// chunk of the tile list, ordered in bands of kBandM tile rows, so the
+// workgroups an XCD runs together share few weight and token tiles.
+__device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int T = tiles_m * tiles_n;
+  const int x = bid % kXcds;
+  const int i = bid / kXcds;
+  const int per = T / kXcds, rem = T % kXcds;
+  const int t = x * per + min(x, rem) + i;
+  const int band = t / (kBandM * tiles_n);
+  const int first = band * kBandM;
+  const int rows = min(tiles_m - first, kBandM);
+  const int in = t - band * kBandM * tiles_n;
+  tm = first + in % rows;
+  tn = in / rows;
+}
+
+struct TileArgs {
+  W8a8Args g;
+  int splits;    // over K, gridDim.y
+  u32* count;    // one arrival counter per wave sub-tile (splits > 1)
+  int* part;     // int32 partials [sub-tile][splits][WI WJ 16][64]
+};
+
+template <int WI, int WJ, bool kSplit>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, WI * WJ >= 8 ? 1 : 2)))
+void w8a8_tile_kernel(const TileArgs p) {
+  constexpr int kTN = 64 * WI, kTM = 64 * WJ;
+  // one LDS object per operand and stage, so the compiler sees that a DMA
+  // into one cannot alias reads of another
+  __shared__ __attribute__((aligned(16))) uint8_t w0[kTN * 128], w1[kTN * 128], a0[kTM * 128], a1[kTM * 128];
+
+  const int M = p.g.M, N = p.g.N, K = p.g.K;
+  int tm, tn;
+  tile_of(blockIdx.x, (M + kTM - 1) / kTM, (N + kTN - 1) / kTN, tm, tn);
+  const int n0 = tn * kTN;
+  const int m0 = tm * kTM;
+  // stages of 128 k; the last one may be half (K % 128 == 64)
+  const int S_all = (K + 127) >> 7;
+  const int q_begin = kSplit ? (int)((long)blockIdx.y * S_all / p.splits) : 0;
+  const int q_end = kSplit ? (int)((long)(blockIdx.y + 1) * S_all / p.splits) : S_all;
+  const bool half_end = q_end == S_all && (K & 64) != 0;
+  const int S = q_end - q_begin - (half_end ? 1 : 0);  // whole stages
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave >> 1;  // n half of the tile
+  const int wm = wave & 1;   // m half of the tile
+  const int l32 = lane & 31;
+  const int lp = lane >> 5;
+
+  // DMA role: instruction k of a wave fills rows 8 (4 k + wave) + lane / 8, slot
+  // lane % 8 of each row, with granule (lane % 8) ^ (row % 8).  Rows past the
+  // end repeat the last row (never stored).  In a half stage the granules of
+  // the missing half repeat those of the first.
+  const uint8_t* wbase = reinterpret_cast<const uint8_t*>(p.g.w) + (size_t)n0 * (size_t)K;
+  const uint8_t* abase = reinterpret_cast<const uint8_t*>(p.g.act) + (size_t)m0 * (size_t)K;
+  const u32 gran = 16u * (u32)((lane & 7) ^ (lane >> 3));
+  const u32 back = (K & 64) != 0 && gran >= 64 ? 64u : 0u;
+  u32 woff[2 * WI], aoff[2 * WJ];
+#pragma unroll
+  for (int k = 0; k < 2 * WI; ++k)
+    woff[k] = (u32)(min(n0 + 8 * (4 * k + wave) + (lane >> 3), N - 1) - n0) * (u32)K + gran;
+#pragma unroll
+  for (int k = 0; k < 2 * WJ; ++k)
+    aoff[k] = (u32)(min(m0 + 8 * (4 * k + wave) + (lane >> 3), M - 1) - m0) * (u32)K + gran;
+  auto dma_stage = [&](int q, auto bc) {  // q counts from q_begin; past the end the last stage again
+    constexpr int b = decltype(bc)::value;
+    const int s = min(q_begin + q, q_end - 1);
+    const u32 col = 128u * (u32)s - (s == S_all - 1 ? back : 0u);
+#pragma unroll
+    for (int k = 0; k < 2 * WI; ++k) dma16(wbase + (woff[k] + col), (b ? w1 : w0) + 1024 * (4 * k + wave));
+#pragma unroll
+    for (int k = 0; k < 2 * WJ; ++k) dma16(abase + (aoff[k] + col), (b ? a1 : a0) + 1024 * (4 * k + wave));
+  };
+
+  // Fragment reads: lane (l32, lp) takes granule 2 ks + lp of rows 32 i + l32 for
+  // k step ks (32 k); half hh holds steps 2 hh and 2 hh + 1.
+  int fo[4];
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) fo[ks] = 128 * l32 + 16 * ((2 * ks + lp) ^ (l32 & 7));
+  const int wrow = wn * 32 * WI * 128, arow = wm * 32 * WJ * 128;
+  struct Frags {
+    v4i w[2][WI], a[2][WJ];
+  };
+  auto read_half = [&](Frags& f, auto bc, auto hc) {
+    constexpr int b = decltype(bc)::value, hh = decltype(hc)::value;
+    const uint8_t* wt = (b ? w1 : w0) + wrow;
+    const uint8_t* at = (b ? a1 : a0) + arow;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int i = 0; i < WI; ++i) f.w[s][i] = *reinterpret_cast<const v4i*>(wt + fo[2 * hh + s] + 4096 * i);
+#pragma unroll
+      for (int j = 0; j < WJ; ++j) f.a[s][j] = *reinterpret_cast<const v4i*>(at + fo[2 * hh + s] + 4096 * j);
+    }
+  };
+
+  v16i acc[WI][WJ];
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+#pragma unroll
+    for (int j = 0; j < WJ; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+  auto mfma_half = [&](const Frags& f) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < WI; ++i)
+#pragma unroll
+        for (int j = 0; j < WJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[s][i], f.a[s][j], acc[i][j], 0, 0, 0);
+  };
+  // one LDS read after each of the first MFMAs of a half
+  auto interleave = [&]() {
+    constexpr int kReads = 2 * (WI + WJ), kMfmas = 2 * WI * WJ;
+#pragma unroll
+    for (int k = 0; k < kReads; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x008, kMfmas >= 2 * kReads ? 1 : 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, kMfmas >= kReads ? 1 : 2, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, kMfmas, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  using B0 = std::integral_constant<int, 0>;
+  using B1 = std::integral_constant<int, 1>;
+  Frags f0, f1;
+  dma_stage(0, B0{});
+  dma_stage(1, B1{});
+  wait_vm_lds<2 * (WI + WJ)>();
+  barrier();
+  read_half(f0, B0{}, B0{});
+  auto iteration = [&](int q, auto bc) {
+    constexpr int b = decltype(bc)::value;
+    using BC = std::integral_constant<int, b>;
+    using BN = std::integral_constant<int, 1 - b>;
+    __builtin_amdgcn_sched_barrier(0);
+    read_half(f1, BC{}, B1{});
+    mfma_half(f0);
+    interleave();
+    wait_vm_lds<0>();  // this wave's reads of the stage, and its DMAs of the next
+    barrier();
+    dma_stage(q + 2, BC{});
+    __builtin_amdgcn_sched_barrier(0);
+    read_half(f0, BN{}, B0{});
+    mfma_half(f1);
+    interleave();
+  };
+  int q = 0;
+  for (; q + 1 < S; q += 2) {
+    iteration(q, B0{});
+    iteration(q + 1, B1{});
+  }
+  if (q < S) iteration(q, B0{});
+  if (half_end) mfma_half(f0);
+  wait_vm_lds<0>();  // no LDS write may land after this
+  barrier();         // every wave has finished its last LDS reads
+
+  if constexpr (kSplit) {
+    // Each wave stores its int32 sub-tile with agent-coherent stores, waits
+    // for them and bumps the sub-tile's counter (which wraps to zero); the
+    // last to arrive adds the others' and runs the epilogue.
+    constexpr int kSub = WI * WJ * 1024;
+    const size_t sub = ((size_t)tm * ((N + kTN - 1) / kTN) + tn) * 4 + wave;
+    int* mine = p.part + (sub * p.splits + blockIdx.y) * kSub + lane;
+#pragma unroll
+    for (int i = 0; i < WI; ++i)
+#pragma unroll
+      for (int j = 0; j < WJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          __hip_atomic_store(mine + (((i * WJ + j) * 16 + e) << 6), acc[i][j][e], __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): the partial is visible to the agent
+    __asm__ volatile("" ::: "memory");
+    u32 old = 0;
+    if (lane == 0) old = atomicInc(p.count + sub, (u32)(p.splits - 1));
+    old = __shfl(old, 0);
+    if (old != (u32)(p.splits - 1)) return;
+    __asm__ volatile("" ::: "memory");
+    for (int s = 0; s < p.splits; ++s) {
+      if (s == (int)blockIdx.y) continue;
+      const int* src = p.part + (sub * p.splits + s) * kSub + lane;
+#pragma unroll
+      for (int i = 0; i < WI; ++i)
+#pragma unroll
+        for (int j = 0; j < WJ; ++j) {
+          v16i t;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            t[e] = __hip_atomic_load(src + (((i * WJ + j) * 16 + e) << 6), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          acc[i][j] += t;
+        }
+    }
+  }
+
+  // y = bf16(epi(acc fl32(s_x s_w) + b)) in fp32 (int32 -> fp32 rounds to 24
+  // bits, far below the bf16 rounding).  The wave writes its 32 WJ x 32 WI
+  // sub-tile to LDS (the stages are free) as rows m of 64 WI bytes, 16-byte
+  // chunk c of row m at chunk c ^ (m % chunks), and stores it in whole row runs.
+  constexpr int kChunks = 4 * WI;
+  uint8_t* stage = wave == 0 ? w0 : wave == 1 ? w1 : wave == 2 ? a0 : a1;
+  float sx[WJ];
+#pragma unroll
+  for (int j = 0; j < WJ; ++j) sx[j] = p.g.act_scales[min(m0 + wm * 32 * WJ + 32 * j + l32, M - 1)];
+#pragma unroll
+  for (int i = 0; i < WI; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int nl = 32 * i + 8 * k + 4 * lp;  // within the wave's columns
+      const int n = n0 + wn * 32 * WI + nl;
+      const int nc = min(n, N - 4);
+      const float4 sw = *reinterpret_cast<const float4*>(p.g.w_scales + nc);
+      float bb[4] = {0.f, 0.f, 0.f, 0.f};
+      if (p.g.bias != nullptr) {
+        const uint2 b2 = *reinterpret_cast<const uint2*>(p.g.bias + nc);
+        bb[0] = bf16_lo(b2.x), bb[1] = bf16_hi(b2.x), bb[2] = bf16_lo(b2.y), bb[3] = bf16_hi(b2.y);
+      }
+#pragma unroll
+      for (int j = 0; j < WJ; ++j) {
+        float o[4] = {(float)acc[i][j][4 * k], (float)acc[i][j][4 * k + 1], (float)acc[i][j][4 * k + 2],
+                      (float)acc[i][j][4 * k + 3]};
+        o[0] = __builtin_fmaf(o[0], sx[j] * sw.x, bb[0]);
+        o[1] = __builtin_fmaf(o[1], sx[j] * sw.y, bb[1]);
+        o[2] = __builtin_fmaf(o[2], sx[j] * sw.z, bb[2]);
+        o[3] = __builtin_fmaf(o[3], sx[j] * sw.w, bb[3]);
+        if (p.g.epilogue == kEpilogueGelu) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) o[v] = gelu_tanh(o[v]);
+        }
+        const int ml = 32 * j + l32;
+        uint8_t* dst = stage + ml * (16 * kChunks) + (((nl >> 3) ^ (ml & (kChunks - 1))) << 4) + 8 * lp;
+        *reinterpret_cast<uint2*>(dst) = uint2{pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3])};
+      }
+    }
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes are done
+  __asm__ volatile("" ::: "memory");
+  const int c = lane & (kChunks - 1);
+  const int n = n0 + wn * 32 * WI + 8 * c;
+  if (n < N) {  // N % 64 == 0: n < N covers n + 7
+    constexpr int kRows = 64 / kChunks;
+#pragma unroll
+    for (int t = 0; t < 32 * WJ / kRows; ++t) {
+      const int ml = kRows * t + lane / kChunks;
+      const int m = m0 + wm * 32 * WJ + ml;
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + ml * (16 * kChunks) + ((c ^ (ml & (kChunks - 1))) << 4));
+      // streaming (non-temporal) stores: Y is not read again by this launch
+      if (m < M)
+        __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p.g.y + (size_t)m * N + n));
+    }
+  }
+}
+
+struct Plan {
+  int wi, wj;   // wave tile in units of 32
+  int tiles;
+  int splits;
+};
+
+// The workgroup tile and the K-splits: the plan whose rounds of workgroups
+// cost least.  A stage of a WI x WJ tile costs its MFMAs or its LDS traffic,
+// whichever is longer, in units of the 32 x 32 x 128 step of a wave.
+Plan plan_of(int64_t M, int64_t N, int64_t K) {
+  const int cus = current_cus();
+  const int S = (int)((K + 127) / 128);
+  static const int shapes[][3] = {{4, 4, 1}, {4, 2, 1}, {2, 2, 2}};  // WI, WJ, workgroups per CU
+  Plan best{};
+  double best_cost = 0;
+  for (const auto& s : shapes) {
+    const int64_t tiles64 = ((N + 64 * s[0] - 1) / (64 * s[0])) * ((M + 64 * s[1] - 1) / (64 * s[1]));
+    if (tiles64 > (1 << 30)) continue;
+    const int tiles = (int)tiles64;
+    const double stage = std::max(4.0 * s[0] * s[1], 1.5 * 2.0 * (s[0] + s[1])) * s[2];
+    for (int splits = 1; splits <= 16 && splits <= S; splits *= 2) {
+      if (splits > 1 && (tiles * 4ll > (int64_t)kWsMaxCounters || tiles >= 2 * cus)) break;
+      const int64_t wgs = (int64_t)tiles * splits;
+      const int64_t rounds = (wgs + (int64_t)cus * s[2] - 1) / ((int64_t)cus * s[2]);
+      const double stages = (double)((S + splits - 1) / splits);
+      const double fill = 2.0 * stage + 3.0 * s[0] * s[1];
+      const double join = splits > 1 ? (6.0 + splits) * s[0] * s[1] : 0.0;
+      const double cost = rounds * (stages * stage + fill + join);
+      if (best.tiles == 0 || cost < best_cost) {
+        best = Plan{s[0], s[1], tiles, splits};
+        best_cost = cost;
+      }
+    }
+  }
+  return best;
+}
+
+template <int WI, int WJ>
+void tile_go(const TileArgs& t, int tiles, hipStream_t stream) {
+  if (t.splits > 1)
+    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, true>), dim3(tiles, t.splits), dim3(kThreads), 0, stream, t);
+  else
+    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, false>), dim3(tiles), dim3(kThreads), 0, stream, t);
+}
+
+}  // namespace
+
+size_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (w8a8_few_tokens(M)) return 0;
+  const Plan p = plan_of(M, N, K);
+  if (p.splits == 1) return 0;
+  return ws_bytes((size_t)p.tiles * 4, (size_t)p.tiles * 4 * p.splits * p.wi * p.wj * 1024 * sizeof(int));
+}
+
+hipError_t launch_w8a8_gemm(const W8a8Args& a, Workspace ws, hipStream_t stream) {
+  if (w8a8_few_tokens(a.M)) return launch_w8a8_skinny(a, stream);
+  const Plan p = plan_of(a.M, a.N, a.K);
+  if (p.splits > 1 && ws.bytes < w8a8_workspace_bytes(a.M, a.N, a.K)) return hipErrorInvalidValue;
+  TileArgs t{a, p.splits, nullptr, nullptr};
+  if (p.splits > 1) {
+    t.count = ws_counters(ws);
+    t.part = static_cast<int*>(ws_scratch(ws));
+  }
+  switch (10 * p.wi + p.wj) {
+    case 44: tile_go<4, 4>(t, p.tiles, stream); break;
+    case 42: tile_go<4, 2>(t, p.tiles, stream); break;
+    case 22: tile_go<2, 2>(t, p.tiles, stream); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace svdq

@@ -450,6 +450,132 @@ svdq_status svdq_awq_w4a16_gemm_stacked(
     int64_t group_size, void* y, void* stream);
 
 /*
+ * 8-bit linear (W8A8): 8-bit weights and activations with one scale per output
+ * channel and one per token, for the projections that stay out of the 4-bit
+ * path (mind-verse.de, "Effiziente Optimierung von Diffusionsmodellen durch
+ * Nunchaku 4-Bit-Quantisierung", section "Nunchaku Lite: Nahtlose Integration in
+ * Diffusers": precision-sensitive layers).  No low-rank branch, no groups.
+ *
+ * svdq_quantize_act_int8, per token m:
+ *   x_hat = x, or with `smooth`  bf16(fl32(x * fl32(1/smooth)))
+ *   s     = fl32(max_k |x_hat| / 127)
+ *   q     = rint_even(x_hat * fl32(1/s))            (the exact product, in [-127, 127])
+ *   A row with fl32(1/s) not finite (all zero, or below about 4e-37) gets codes
+ *   0; a row that holds an infinity or NaN gets codes 0 and s = NaN, so that its
+ *   row of Y is NaN and no other row is touched.  Codes and scales are exactly
+ *   defined.
+ *   x device bf16 [M, K]; smooth device fp32 [K] or NULL
+ *   act_codes device out int8 [M, K]; act_scales device out fp32 [M]
+ *
+ * svdq_w8a8_gemm:
+ *   Y[m,n] = bf16( epi( (sum_k q_x[m,k] q_w[n,k]) * fl32(s_x[m] s_w[n]) + bias[n] ) )
+ *   the sum exact in int32 (any codes, -128 included), one fp32 fma, epi none or
+ *   GELU (svdq_epilogue), one bf16 rounding.
+ *   act_codes int8 [M, K], act_scales fp32 [M], w_codes int8 [N, K], w_scales
+ *   fp32 [N] (svdq_pack_weights_int8), bias bf16 [N] or NULL, y bf16 [M, N]
+ *   workspace of svdq_w8a8_gemm_workspace_size(M, N, K) bytes (see Conventions):
+ *   with few output tiles K is split over workgroups, whose int32 partials meet
+ *   there; being integers, their sum does not depend on the order.
+ * K % 64 == 0, N % 64 == 0, M <= 2^24, N <= 2^20, K <= 65536 (NOT_SUPPORTED
+ * beyond); M == 0 is a no-op; other errors as for svdq_w4a4_gemm_lora_up_ex.
+ */
+svdq_status svdq_quantize_act_int8(const void* x, const float* smooth, int64_t M, int64_t K,
+                                   int8_t* act_codes, float* act_scales, void* stream);
+svdq_status svdq_w8a8_gemm(const int8_t* act_codes, const float* act_scales, const int8_t* w_codes,
+                           const float* w_scales, const void* bias, int64_t M, int64_t N, int64_t K,
+                           int epilogue, void* y, void* workspace, size_t workspace_bytes, void* stream);
+size_t svdq_w8a8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/*
+ * The norms before and after a block, fused with its gate and the residual
+ * scale.  Adaptive-normalization blocks of a diffusion transformer take gate,
+ * scale and shift from the modulation projections (mind-verse.de, same page and
+ * section, modulation layers).  Per row m of C channels:
+ *   u = y, or  post_norm(y) * post_weight
+ *   h = residual_scale * x + gate * u                  (with y; without it h = x)
+ *   z = norm(h) * weight * (1 + scale) + shift         (norm not SVDQ_NORM_NONE)
+ *   RMS norm: v / sqrt(mean(v^2) + eps); layer norm: the same of v - mean(v).
+ * All in fp32, z from the unrounded h; a vector that is NULL drops out (gate and
+ * the weights as 1, scale and shift as 0).  z leaves as bf16, or with
+ * SVDQ_NORM_OUT_INT8 as the codes and token scales that svdq_w8a8_gemm reads:
+ * those of svdq_quantize_act_int8 for v = fl32(z fl32(1/smooth)) (or z) in the
+ * place of x_hat, not rounded to bf16 in between.
+ *
+ *   x            device, bf16 or fp32 (stream_type) [M, C], rows x_stride apart
+ *   y            device, bf16 [M, C], rows y_stride apart, or NULL (then no h)
+ *   post_weight  device, bf16 [C] or NULL (needs a post norm)
+ *   gate         device, bf16 [gate_rows, C], rows gate_stride apart, or NULL
+ *   scale, shift device, bf16 [mod_rows, C], rows mod_stride apart, or NULL each
+ *                (one row serves as the norm's bias); gate_rows and mod_rows
+ *                divide M: row m takes row m / (M / rows)
+ *   weight       device, bf16 [C] or NULL
+ *   h            device out, x's type [M, C], rows h_stride apart; may be x itself
+ *                with x's stride (the stream updated in place)
+ *   z            device out, bf16 [M, C] or int8 [M, C]; z_scales fp32 [M] for int8
+ *   smooth       device, fp32 [C] or NULL (int8 output only)
+ * Strides are in elements and multiples of 8 (the chunks of a modulation
+ * projection's output are rows of a larger stride); strides of arrays with one
+ * row are not read.  C % 8 == 0, C % 64 == 0 for int8, C <= 32768, M <= 2^24
+ * (NOT_SUPPORTED beyond); M == 0 is a no-op; INVALID_VALUE for an unknown enum
+ * value, a vector without the part it belongs to, a bad eps or
+ * residual_scale, rows that do not divide M, and as for the other calls.
+ */
+typedef enum { SVDQ_NORM_NONE = 0, SVDQ_NORM_LAYER = 1, SVDQ_NORM_RMS = 2 } svdq_norm;
+typedef enum { SVDQ_STREAM_BF16 = 0, SVDQ_STREAM_FP32 = 1 } svdq_stream_type;
+typedef enum { SVDQ_NORM_OUT_BF16 = 0, SVDQ_NORM_OUT_INT8 = 1 } svdq_norm_out;
+svdq_status svdq_gate_norm_modulate(
+    const void* x, int stream_type, int64_t x_stride, const void* y, int64_t y_stride,
+    int post_norm, const void* post_weight, const void* gate, int64_t gate_rows, int64_t gate_stride,
+    float residual_scale, int norm, const void* weight, const void* scale, const void* shift,
+    int64_t mod_rows, int64_t mod_stride, float eps, int64_t M, int64_t C,
+    void* h, int64_t h_stride, int out_type, const float* smooth, void* z, float* z_scales, void* stream);
+
+/*
+ * Rotary positions with several axes (time, height, width, ...).  A token has
+ * one position per axis, axis a turns axes[a] channels (even), R = sum(axes):
+ *   angle_i = position[axis of i] * rate_i,   i = 0 .. R/2 - 1, axis by axis
+ *   rate_i  = theta^(-2 j / axes[a])  for the j-th angle of axis a (SVDQ_SPECTRUM_AXIS)
+ *           = theta^(-2 i / R)                                     (SVDQ_SPECTRUM_SHARED)
+ * The product and its reduction are done in double, so far positions keep
+ * their precision.
+ *
+ * svdq_rope_axes_tables writes cos and sin, fp32 [M, R/2]: with R = 128 the
+ * tables of svdq_w4a4_gemm_qkv_norm_rope.
+ *
+ * svdq_rope_axes turns Q and K, token by token, all heads by the same angles:
+ *   v = q head, or with q_norm  q / sqrt(mean(q^2) + eps) * q_norm   (per head)
+ *   SVDQ_ROPE_PAIRS:  (v[2i], v[2i+1]) -> (v[2i] c - v[2i+1] s, v[2i] s + v[2i+1] c)
+ *   SVDQ_ROPE_HALVES: the same of (v[i], v[i + R/2])
+ *   channels R .. head_dim - 1 are not turned (but normed)
+ * in fp32, rounded to bf16 once.
+ *
+ *   q, k       device, bf16 [M, heads, head_dim], tokens q_stride / k_stride
+ *              elements apart (multiples of 8; the thirds of a fused QKV output);
+ *              k may be NULL with k_heads == 0
+ *   positions  device, fp32 or int32 (position_type) [position_rows, n_axes];
+ *              position_rows divides M, token m reads row m % position_rows
+ *              (a batch that shares its positions)
+ *   axes       HOST array of n_axes widths; at most 8 axes, R <= 256 and <= head_dim
+ *   q_norm, k_norm  device, bf16 [head_dim], both or neither; eps finite, >= 0
+ *   q_out, k_out    device out, as q and k, strides of their own; may be q and k
+ *              themselves with the same strides (in place)
+ * head_dim % 8 == 0 and <= 256; for SVDQ_ROPE_HALVES R % 8 == 0; at most 4096 heads
+ * each, M <= 2^24 (NOT_SUPPORTED beyond); theta finite and > 1; M == 0 is a no-op.
+ */
+typedef enum { SVDQ_POSITIONS_FP32 = 0, SVDQ_POSITIONS_INT32 = 1 } svdq_position_type;
+typedef enum { SVDQ_SPECTRUM_AXIS = 0, SVDQ_SPECTRUM_SHARED = 1 } svdq_spectrum;
+typedef enum { SVDQ_ROPE_PAIRS = 0, SVDQ_ROPE_HALVES = 1 } svdq_rope_layout;
+svdq_status svdq_rope_axes_tables(const void* positions, int position_type, int64_t M, int64_t n_axes,
+                                  const int64_t* axes, double theta, int spectrum, float* rope_cos,
+                                  float* rope_sin, void* stream);
+svdq_status svdq_rope_axes(
+    const void* q, int64_t q_stride, int64_t q_heads, const void* k, int64_t k_stride, int64_t k_heads,
+    int64_t head_dim, int64_t M, const void* positions, int position_type, int64_t position_rows,
+    int64_t n_axes, const int64_t* axes, double theta, int spectrum, int layout,
+    const void* q_norm, const void* k_norm, float eps, void* q_out, int64_t q_out_stride,
+    void* k_out, int64_t k_out_stride, void* stream);
+
+/*
  * Host-side packer, step 1: the smoothing vector (mind-verse.de, section
  * "Nunchaku und SVDQuant": outliers of the activations are shifted into the
  * weights).  lambda_j = fl32(sqrt(max(a_j, 1e-5) / max(max_n |W_nj|, 1e-5))),
@@ -497,6 +623,18 @@ svdq_status svdq_pack_weights(const uint16_t* w, const float* smooth,
 svdq_status svdq_pack_weights_fp4(const uint16_t* w, const float* smooth, int64_t N, int64_t K, int64_t r,
                                   uint64_t seed, uint8_t* w_codes, uint8_t* w_scales, uint16_t* lora_down,
                                   uint16_t* lora_up);
+
+/*
+ * Host packer of the 8-bit linear: W' = W diag(smooth) in double (smooth NULL:
+ * W), per output channel s = fl32(max_k |W'| / 127) and
+ * q = clamp(rint_even(W' / s), -127, 127), a zero row s = 0 and codes 0.
+ *   w host bf16 [N, K]; smooth host fp32 [K] or NULL; N, K > 0
+ *   w_codes host out int8 [N, K]; w_scales host out fp32 [N]
+ * A weight or product that is not finite is INVALID_VALUE.  CPU only (threads);
+ * deterministic.
+ */
+svdq_status svdq_pack_weights_int8(const uint16_t* w, const float* smooth, int64_t N, int64_t K,
+                                   int8_t* w_codes, float* w_scales);
 
 /*
  * Host AWQ packer (CPU, caller-owned host buffers): the offline step of the

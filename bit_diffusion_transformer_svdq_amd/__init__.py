@@ -42,14 +42,14 @@ __all__ = ["SvdqError", "lib", "check_device", "quantize_act_lora_down", "w4a4_g
            "quantize_act_lora_down_fp4", "fp4_gemm_lora_up", "pack_weights_fp4",
            "release_workspaces", "GROUP_SIZE",
            "quantize_act_int8", "w8a8_gemm", "pack_weights_int8", "gate_norm_modulate", "rope_axes",
-           "rope_axes_tables"]
+           "rope_axes_tables", "debug_set_w8a8_plan"]
 
 GROUP_SIZE = 64
 
 # the block operators live in block.py, which needs torch; it is imported when
 # one of them is first used
 _BLOCK = ("quantize_act_int8", "w8a8_gemm", "pack_weights_int8", "gate_norm_modulate", "rope_axes",
-          "rope_axes_tables")
+          "rope_axes_tables", "debug_set_w8a8_plan")
 
 
 def __getattr__(name):

@@ -67,6 +67,7 @@ SIGNATURES = {
         _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, ctypes.c_int,
         _c_void_p, _c_void_p, _size, _c_void_p]),
     "svdq_w8a8_gemm_workspace_size": (_size, [_i64, _i64, _i64]),
+    "svdq_debug_set_w8a8_plan": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
     "svdq_gate_norm_modulate": (ctypes.c_int, [
         _c_void_p, ctypes.c_int, _i64, _c_void_p, _i64, ctypes.c_int, _c_void_p, _c_void_p, _i64, _i64,
         ctypes.c_float, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, ctypes.c_float, _i64, _i64,

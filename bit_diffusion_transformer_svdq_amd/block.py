@@ -131,6 +131,11 @@ def w8a8_gemm(act_codes, act_scales, w_codes, w_scales, bias=None, out=None, str
     return y
 
 
+def debug_set_w8a8_plan(tile: int = 0, splits: int = 0) -> None:
+    """Test hook: w8a8_gemm's kernel and K-splits for later calls (0 = by shape)."""
+    check(lib().svdq_debug_set_w8a8_plan(int(tile), int(splits)), "svdq_debug_set_w8a8_plan")
+
+
 def gate_norm_modulate(x, y=None, post_norm="none", post_weight=None, gate=None, residual_scale=1.0, norm="layer",
                        weight=None, scale=None, shift=None, eps=1e-6, quantize=None, smooth=None, h_out=None,
                        out=None, stream=None):

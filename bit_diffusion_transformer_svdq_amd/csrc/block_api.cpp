@@ -118,6 +118,14 @@ size_t svdq_w8a8_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
   return svdq::w8a8_workspace_bytes(M, N, K);
 }
 
+svdq_status svdq_debug_set_w8a8_plan(int tile, int splits) {
+  if (tile != 0 && tile != 1 && tile != 22 && tile != 42 && tile != 43 && tile != 34 && tile != 44)
+    return fail(SVDQ_STATUS_INVALID_VALUE, "bad w8a8 tile %d (0, 1, 22, 42, 43, 34 or 44)", tile);
+  if (splits < 0 || splits > 16) return fail(SVDQ_STATUS_INVALID_VALUE, "bad split count %d (0..16)", splits);
+  svdq::set_w8a8_plan_override(tile, splits);
+  return ok();
+}
+
 svdq_status svdq_w8a8_gemm(const int8_t* act_codes, const float* act_scales, const int8_t* w_codes,
                            const float* w_scales, const void* bias, int64_t M, int64_t N, int64_t K, int epilogue,
                            void* y, void* workspace, size_t workspace_bytes, void* stream) {

@@ -20,8 +20,10 @@
 //    issued, and while the second half's MFMAs run the first half of stage
 //    q + 1 is read.  One barrier per stage, with a whole stage of MFMAs between
 //    a DMA and the wait for it;
-//  * 16-byte granule g of row R sits at slot 8 R + (g ^ R[2:0]): the 8 rows of a
-//    fragment-read phase take all 32 banks;
+//  * 16-byte granule g of row R sits at slot 8 R + (g ^ R[3:1]).  A 16-byte LDS
+//    read runs in phases of 16 lanes (0-3, 12-15, 20-23, 24-27; 4-11, 16-19, 28-31;
+//    the same in the upper half) over 256 bytes of banks: in each phase the even
+//    and the odd rows then take 8 different slots, no two lanes one bank;
 //  * few tiles: K is split over workgroups, whose int32 partials meet in the
 //    caller's workspace (integer sums: the order does not matter).
 //
@@ -33,6 +35,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "row_device.h"
@@ -48,7 +51,6 @@ typedef unsigned int u32;
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) void glb_void;
 
-constexpr int kThreads = 256;  // 4 waves
 constexpr int kXcds = 8;
 constexpr int kBandM = 4;
 
@@ -97,10 +99,27 @@ struct TileArgs {
   int* part;     // int32 partials [sub-tile][splits][WI WJ 16][64]
 };
 
-template <int WI, int WJ, bool kSplit>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, WI * WJ >= 8 ? 1 : 2)))
-void w8a8_tile_kernel(const TileArgs p) {
-  constexpr int kTN = 64 * WI, kTM = 64 * WJ;
+// GELU (tanh form) as x - x / (exp(2u) + 1) with exp(2u) = 2^(x (c0 + c1 x^2)): one
+// exponential and one reciprocal, five other operations; within 2^-21 |x|
+__device__ __forceinline__ float gelu_exp2(float x) {
+  constexpr float c0 = 2.302208198f, c1 = 0.1029432397f;  // 2 sqrt(2/pi) log2(e), and 0.044715 times it
+  const float e = __builtin_amdgcn_exp2f(x * __builtin_fmaf(c1, x * x, c0));
+  return __builtin_fmaf(-x, __builtin_amdgcn_rcpf(e + 1.0f), x);
+}
+
+// WN x WM waves of WI x WJ tiles of 32 x 32
+template <int WI, int WJ, int WN, int WM>
+struct Shape {
+  static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves;
+  static constexpr int kTN = 32 * WI * WN, kTM = 32 * WJ * WM;
+  static constexpr int kWgs = 2 * 128 * (kTN + kTM) > 80 * 1024 ? 1 : 2;  // per CU, by LDS
+  static constexpr int kSub = WI * WJ * 1024;                             // accumulators of a wave
+};
+
+template <int WI, int WJ, int WN, int WM, bool kSplit>
+__global__ __launch_bounds__((Shape<WI, WJ, WN, WM>::kThreads), 2) void w8a8_tile_kernel(const TileArgs p) {
+  using Sh = Shape<WI, WJ, WN, WM>;
+  constexpr int kTN = Sh::kTN, kTM = Sh::kTM, kWaves = Sh::kWaves;
   // one LDS object per operand and stage, so the compiler sees that a DMA
   // into one cannot alias reads of another
   __shared__ __attribute__((aligned(16))) uint8_t w0[kTN * 128], w1[kTN * 128], a0[kTM * 128], a1[kTM * 128];
@@ -120,41 +139,52 @@ void w8a8_tile_kernel(const TileArgs p) {
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wn = wave >> 1;  // n half of the tile
-  const int wm = wave & 1;   // m half of the tile
+  const int wn = wave / WM;
+  const int wm = wave % WM;
   const int l32 = lane & 31;
   const int lp = lane >> 5;
 
-  // DMA role: instruction k of a wave fills rows 8 (4 k + wave) + lane / 8, slot
-  // lane % 8 of each row, with granule (lane % 8) ^ (row % 8).  Rows past the
+  // DMA role: instruction k of a wave fills rows 8 (waves k + wave) + lane / 8, slot
+  // lane % 8 of each row, with granule (lane % 8) ^ row[3:1].  Rows past the
   // end repeat the last row (never stored).  In a half stage the granules of
   // the missing half repeat those of the first.
   const uint8_t* wbase = reinterpret_cast<const uint8_t*>(p.g.w) + (size_t)n0 * (size_t)K;
   const uint8_t* abase = reinterpret_cast<const uint8_t*>(p.g.act) + (size_t)m0 * (size_t)K;
-  const u32 gran = 16u * (u32)((lane & 7) ^ (lane >> 3));
+  const u32 gran = 16u * (u32)((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));
   const u32 back = (K & 64) != 0 && gran >= 64 ? 64u : 0u;
-  u32 woff[2 * WI], aoff[2 * WJ];
+  constexpr int kWd = kTN / (8 * kWaves), kAd = kTM / (8 * kWaves);  // DMAs per stage and wave
+  static_assert(kWaves % 2 == 0 && kWd * 8 * kWaves == kTN && kAd * 8 * kWaves == kTM, "whole row runs per wave");
+  u32 woff[kWd], aoff[kAd];
 #pragma unroll
-  for (int k = 0; k < 2 * WI; ++k)
-    woff[k] = (u32)(min(n0 + 8 * (4 * k + wave) + (lane >> 3), N - 1) - n0) * (u32)K + gran;
+  for (int k = 0; k < kWd; ++k)
+    woff[k] = (u32)(min(n0 + 8 * (kWaves * k + wave) + (lane >> 3), N - 1) - n0) * (u32)K + gran;
 #pragma unroll
-  for (int k = 0; k < 2 * WJ; ++k)
-    aoff[k] = (u32)(min(m0 + 8 * (4 * k + wave) + (lane >> 3), M - 1) - m0) * (u32)K + gran;
-  auto dma_stage = [&](int q, auto bc) {  // q counts from q_begin; past the end the last stage again
-    constexpr int b = decltype(bc)::value;
+  for (int k = 0; k < kAd; ++k)
+    aoff[k] = (u32)(min(m0 + 8 * (kWaves * k + wave) + (lane >> 3), M - 1) - m0) * (u32)K + gran;
+  // column of stage q (counted from q_begin; past the end the last stage again)
+  auto stage_col = [&](int q) {
     const int s = min(q_begin + q, q_end - 1);
-    const u32 col = 128u * (u32)s - (s == S_all - 1 ? back : 0u);
+    return 128u * (u32)s - (s == S_all - 1 ? back : 0u);
+  };
+  constexpr int kDmas = kWd + kAd;
+  auto dma_one = [&](int k, u32 col, auto bc) {
+    constexpr int b = decltype(bc)::value;
+    if (k < kWd)
+      dma16(wbase + (woff[k] + col), (b ? w1 : w0) + 1024 * (kWaves * k + wave));
+    else
+      dma16(abase + (aoff[k - kWd] + col), (b ? a1 : a0) + 1024 * (kWaves * (k - kWd) + wave));
+  };
+  auto dma_stage = [&](int q, auto bc) {
+    const u32 col = stage_col(q);
 #pragma unroll
-    for (int k = 0; k < 2 * WI; ++k) dma16(wbase + (woff[k] + col), (b ? w1 : w0) + 1024 * (4 * k + wave));
-#pragma unroll
-    for (int k = 0; k < 2 * WJ; ++k) dma16(abase + (aoff[k] + col), (b ? a1 : a0) + 1024 * (4 * k + wave));
+    for (int k = 0; k < kDmas; ++k) dma_one(k, col, bc);
   };
 
   // Fragment reads: lane (l32, lp) takes granule 2 ks + lp of rows 32 i + l32 for
   // k step ks (32 k); half hh holds steps 2 hh and 2 hh + 1.
   int fo[4];
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) fo[ks] = 128 * l32 + 16 * ((2 * ks + lp) ^ (l32 & 7));
+  for (int ks = 0; ks < 4; ++ks) fo[ks] = 128 * l32 + 16 * ((2 * ks + lp) ^ ((l32 >> 1) & 7));
   const int wrow = wn * 32 * WI * 128, arow = wm * 32 * WJ * 128;
   struct Frags {
     v4i w[2][WI], a[2][WJ];
@@ -188,15 +218,21 @@ void w8a8_tile_kernel(const TileArgs p) {
         for (int j = 0; j < WJ; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[s][i], f.a[s][j], acc[i][j], 0, 0, 0);
   };
-  // one LDS read after each of the first MFMAs of a half
-  auto interleave = [&]() {
+  // One LDS read (two where there are more of them than MFMAs) after each of
+  // the first MFMAs of a half; in the second half the DMAs are spread over the
+  // MFMAs, so that the waves do not queue for the address unit while the matrix
+  // core idles.
+  auto interleave = [&](auto with_dma) {
     constexpr int kReads = 2 * (WI + WJ), kMfmas = 2 * WI * WJ;
+    constexpr int kRead = (kReads + kMfmas - 1) / kMfmas;
+    constexpr int kEvery = kMfmas / kDmas > 0 ? kMfmas / kDmas : 1, kDma = (kDmas * kEvery + kMfmas - 1) / kMfmas;
 #pragma unroll
-    for (int k = 0; k < kReads; ++k) {
-      __builtin_amdgcn_sched_group_barrier(0x008, kMfmas >= 2 * kReads ? 1 : 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, kMfmas >= kReads ? 1 : 2, 0);
+    for (int k = 0; k < kMfmas; ++k) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (k * kRead < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kRead, 0);
+      if constexpr (decltype(with_dma)::value)
+        if (k % kEvery == kEvery - 1) __builtin_amdgcn_sched_group_barrier(0x020, kDma, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, kMfmas, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
 
@@ -205,7 +241,7 @@ void w8a8_tile_kernel(const TileArgs p) {
   Frags f0, f1;
   dma_stage(0, B0{});
   dma_stage(1, B1{});
-  wait_vm_lds<2 * (WI + WJ)>();
+  wait_vm_lds<kDmas>();
   barrier();
   read_half(f0, B0{}, B0{});
   auto iteration = [&](int q, auto bc) {
@@ -215,14 +251,16 @@ void w8a8_tile_kernel(const TileArgs p) {
     __builtin_amdgcn_sched_barrier(0);
     read_half(f1, BC{}, B1{});
     mfma_half(f0);
-    interleave();
+    interleave(B0{});
+    const u32 col = stage_col(q + 2);
     wait_vm_lds<0>();  // this wave's reads of the stage, and its DMAs of the next
     barrier();
-    dma_stage(q + 2, BC{});
     __builtin_amdgcn_sched_barrier(0);
     read_half(f0, BN{}, B0{});
+#pragma unroll
+    for (int k = 0; k < kDmas; ++k) dma_one(k, col, bc);
     mfma_half(f1);
-    interleave();
+    interleave(B1{});
   };
   int q = 0;
   for (; q + 1 < S; q += 2) {
@@ -238,8 +276,8 @@ void w8a8_tile_kernel(const TileArgs p) {
     // Each wave stores its int32 sub-tile with agent-coherent stores, waits
     // for them and bumps the sub-tile's counter (which wraps to zero); the
     // last to arrive adds the others' and runs the epilogue.
-    constexpr int kSub = WI * WJ * 1024;
-    const size_t sub = ((size_t)tm * ((N + kTN - 1) / kTN) + tn) * 4 + wave;
+    constexpr int kSub = Sh::kSub;
+    const size_t sub = ((size_t)tm * ((N + kTN - 1) / kTN) + tn) * kWaves + wave;
     int* mine = p.part + (sub * p.splits + blockIdx.y) * kSub + lane;
 #pragma unroll
     for (int i = 0; i < WI; ++i)
@@ -275,20 +313,24 @@ void w8a8_tile_kernel(const TileArgs p) {
 
   // y = bf16(epi(acc fl32(s_x s_w) + b)) in fp32 (int32 -> fp32 rounds to 24
   // bits, far below the bf16 rounding).  The wave writes its 32 WJ x 32 WI
-  // sub-tile to LDS (the stages are free) as rows m of 64 WI bytes, 16-byte
-  // chunk c of row m at chunk c ^ (m % chunks), and stores it in whole row runs.
-  constexpr int kChunks = 4 * WI;
-  uint8_t* stage = wave == 0 ? w0 : wave == 1 ? w1 : wave == 2 ? a0 : a1;
+  // sub-tile to LDS (the stages are free) as rows m of 64 WI bytes, and stores
+  // it from there in row runs.
+  constexpr int kChunks = 4 * WI;                    // 16-byte chunks of a sub-tile row
+  constexpr int kMask = kChunks % 8 == 0 ? 7 : 3;    // chunk c of row m sits at c ^ (m & kMask)
+  constexpr int kPerBuf = kWaves / 4;                // waves that share a stage buffer
+  static_assert(kPerBuf * 2 * Sh::kSub <= 128 * (kTN < kTM ? kTN : kTM), "sub-tiles fit the stages");
+  const int sb = wave / kPerBuf;
+  uint8_t* stage = (sb == 0 ? w0 : sb == 1 ? w1 : sb == 2 ? a0 : a1) + (wave % kPerBuf) * 2 * Sh::kSub;
+  const int nw = n0 + wn * 32 * WI, mw = m0 + wm * 32 * WJ;  // the wave's first column and row
   float sx[WJ];
 #pragma unroll
-  for (int j = 0; j < WJ; ++j) sx[j] = p.g.act_scales[min(m0 + wm * 32 * WJ + 32 * j + l32, M - 1)];
+  for (int j = 0; j < WJ; ++j) sx[j] = p.g.act_scales[min(mw + 32 * j + l32, M - 1)];
 #pragma unroll
   for (int i = 0; i < WI; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int nl = 32 * i + 8 * k + 4 * lp;  // within the wave's columns
-      const int n = n0 + wn * 32 * WI + nl;
-      const int nc = min(n, N - 4);
+      const int nc = min(nw + nl, N - 4);
       const float4 sw = *reinterpret_cast<const float4*>(p.g.w_scales + nc);
       float bb[4] = {0.f, 0.f, 0.f, 0.f};
       if (p.g.bias != nullptr) {
@@ -305,61 +347,78 @@ void w8a8_tile_kernel(const TileArgs p) {
         o[3] = __builtin_fmaf(o[3], sx[j] * sw.w, bb[3]);
         if (p.g.epilogue == kEpilogueGelu) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) o[v] = gelu_tanh(o[v]);
+          for (int v = 0; v < 4; ++v) o[v] = gelu_exp2(o[v]);
         }
         const int ml = 32 * j + l32;
-        uint8_t* dst = stage + ml * (16 * kChunks) + (((nl >> 3) ^ (ml & (kChunks - 1))) << 4) + 8 * lp;
+        uint8_t* dst = stage + ml * (16 * kChunks) + (((nl >> 3) ^ (ml & kMask)) << 4) + 8 * lp;
         *reinterpret_cast<uint2*>(dst) = uint2{pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3])};
       }
     }
   __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes are done
   __asm__ volatile("" ::: "memory");
-  const int c = lane & (kChunks - 1);
-  const int n = n0 + wn * 32 * WI + 8 * c;
-  if (n < N) {  // N % 64 == 0: n < N covers n + 7
-    constexpr int kRows = 64 / kChunks;
+  // chunk by chunk in row order: an instruction stores 64 chunks, whole rows of
+  // 64 WI bytes where they divide 64
 #pragma unroll
-    for (int t = 0; t < 32 * WJ / kRows; ++t) {
-      const int ml = kRows * t + lane / kChunks;
-      const int m = m0 + wm * 32 * WJ + ml;
-      const uint4 v = *reinterpret_cast<const uint4*>(stage + ml * (16 * kChunks) + ((c ^ (ml & (kChunks - 1))) << 4));
-      // streaming (non-temporal) stores: Y is not read again by this launch
-      if (m < M)
-        __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p.g.y + (size_t)m * N + n));
-    }
+  for (int t = 0; t < 32 * WJ * kChunks / 64; ++t) {
+    const int at = 64 * t + lane;
+    const int ml = at / kChunks, c = at - ml * kChunks;
+    const int m = mw + ml, n = nw + 8 * c;
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + ml * (16 * kChunks) + ((c ^ (ml & kMask)) << 4));
+    // streaming (non-temporal) stores: Y is not read again by this launch;
+    // N % 64 == 0, so n < N covers n + 7
+    if (m < M && n < N)
+      __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p.g.y + (size_t)m * N + n));
   }
 }
 
 struct Plan {
-  int wi, wj;   // wave tile in units of 32
+  int shape;    // index into kShapes
   int tiles;
   int splits;
 };
 
+struct ShapeInfo {
+  int code;     // the test hook's name
+  int tn, tm, waves, wgs, sub;
+  double stage; // cost of a 128-wide k stage of one workgroup, in matrix-core cycles of a CU
+};
+template <int WI, int WJ, int WN, int WM>
+constexpr ShapeInfo info(int code, double stage) {
+  using S = Shape<WI, WJ, WN, WM>;
+  return ShapeInfo{code, S::kTN, S::kTM, S::kWaves, S::kWgs, S::kSub, stage};
+}
+constexpr ShapeInfo kShapes[] = {info<4, 2, 2, 4>(44, 2048), info<3, 2, 2, 4>(34, 1536), info<2, 3, 4, 2>(43, 1536),
+                                 info<2, 2, 4, 2>(42, 1100), info<2, 2, 2, 2>(22, 620)};
+
+std::atomic<int> g_tile{0}, g_splits{0};  // test hook
+
 // The workgroup tile and the K-splits: the plan whose rounds of workgroups
-// cost least.  A stage of a WI x WJ tile costs its MFMAs or its LDS traffic,
-// whichever is longer, in units of the 32 x 32 x 128 step of a wave.
+// cost least.
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int cus = current_cus();
   const int S = (int)((K + 127) / 128);
-  static const int shapes[][3] = {{4, 4, 1}, {4, 2, 1}, {2, 2, 2}};  // WI, WJ, workgroups per CU
-  Plan best{};
+  Plan best{-1, 0, 1};
   double best_cost = 0;
-  for (const auto& s : shapes) {
-    const int64_t tiles64 = ((N + 64 * s[0] - 1) / (64 * s[0])) * ((M + 64 * s[1] - 1) / (64 * s[1]));
+  const int forced_tile = g_tile.load(std::memory_order_relaxed), forced = g_splits.load(std::memory_order_relaxed);
+  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
+    const ShapeInfo& s = kShapes[i];
+    if (forced_tile > 1 && forced_tile != s.code) continue;
+    const int64_t tiles64 = ((N + s.tn - 1) / s.tn) * ((M + s.tm - 1) / s.tm);
     if (tiles64 > (1 << 30)) continue;
     const int tiles = (int)tiles64;
-    const double stage = std::max(4.0 * s[0] * s[1], 1.5 * 2.0 * (s[0] + s[1])) * s[2];
     for (int splits = 1; splits <= 16 && splits <= S; splits *= 2) {
-      if (splits > 1 && (tiles * 4ll > (int64_t)kWsMaxCounters || tiles >= 2 * cus)) break;
-      const int64_t wgs = (int64_t)tiles * splits;
-      const int64_t rounds = (wgs + (int64_t)cus * s[2] - 1) / ((int64_t)cus * s[2]);
+      if (splits > 1 && (tiles * (int64_t)s.waves > (int64_t)kWsMaxCounters || (tiles >= 2 * cus && forced <= 1))) break;
+      if (forced > 0 && splits != forced && 2 * splits <= std::min(16, S) && splits < forced) continue;
+      if (forced > 0 && splits > forced) break;
+      const int64_t wgs = (int64_t)tiles * splits, slots = (int64_t)cus * s.wgs;
+      const int64_t rounds = (wgs + slots - 1) / slots;
       const double stages = (double)((S + splits - 1) / splits);
-      const double fill = 2.0 * stage + 3.0 * s[0] * s[1];
-      const double join = splits > 1 ? (6.0 + splits) * s[0] * s[1] : 0.0;
-      const double cost = rounds * (stages * stage + fill + join);
-      if (best.tiles == 0 || cost < best_cost) {
-        best = Plan{s[0], s[1], tiles, splits};
+      const double area = s.tn * s.tm / 65536.0;
+      const double fill = 3000 + 16000 * area;
+      const double join = splits > 1 ? 3000 + (6000.0 + 3000.0 * splits) * area : 0.0;
+      const double cost = rounds * s.wgs * (stages * s.stage + fill + join);
+      if (best.shape < 0 || cost < best_cost) {
+        best = Plan{i, tiles, splits};
         best_cost = cost;
       }
     }
@@ -367,25 +426,38 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
-template <int WI, int WJ>
+template <int WI, int WJ, int WN, int WM>
 void tile_go(const TileArgs& t, int tiles, hipStream_t stream) {
+  const dim3 block(Shape<WI, WJ, WN, WM>::kThreads);
   if (t.splits > 1)
-    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, true>), dim3(tiles, t.splits), dim3(kThreads), 0, stream, t);
+    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, WN, WM, true>), dim3(tiles, t.splits), block, 0, stream, t);
   else
-    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, false>), dim3(tiles), dim3(kThreads), 0, stream, t);
+    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, WN, WM, false>), dim3(tiles), block, 0, stream, t);
 }
 
 }  // namespace
 
+void set_w8a8_plan_override(int tile, int splits) {
+  g_tile.store(tile, std::memory_order_relaxed);
+  g_splits.store(splits, std::memory_order_relaxed);
+}
+
+// up to 64 tokens run on the weight-streaming kernel
+static bool few_tokens(int64_t M) {
+  const int t = g_tile.load(std::memory_order_relaxed);
+  return M <= 64 && t <= 1;
+}
+
 size_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (w8a8_few_tokens(M)) return 0;
+  if (few_tokens(M)) return 0;
   const Plan p = plan_of(M, N, K);
   if (p.splits == 1) return 0;
-  return ws_bytes((size_t)p.tiles * 4, (size_t)p.tiles * 4 * p.splits * p.wi * p.wj * 1024 * sizeof(int));
+  const ShapeInfo& s = kShapes[p.shape];
+  return ws_bytes((size_t)p.tiles * s.waves, (size_t)p.tiles * s.waves * p.splits * s.sub * sizeof(int));
 }
 
 hipError_t launch_w8a8_gemm(const W8a8Args& a, Workspace ws, hipStream_t stream) {
-  if (w8a8_few_tokens(a.M)) return launch_w8a8_skinny(a, stream);
+  if (few_tokens(a.M)) return launch_w8a8_skinny(a, stream);
   const Plan p = plan_of(a.M, a.N, a.K);
   if (p.splits > 1 && ws.bytes < w8a8_workspace_bytes(a.M, a.N, a.K)) return hipErrorInvalidValue;
   TileArgs t{a, p.splits, nullptr, nullptr};
@@ -393,10 +465,12 @@ hipError_t launch_w8a8_gemm(const W8a8Args& a, Workspace ws, hipStream_t stream)
     t.count = ws_counters(ws);
     t.part = static_cast<int*>(ws_scratch(ws));
   }
-  switch (10 * p.wi + p.wj) {
-    case 44: tile_go<4, 4>(t, p.tiles, stream); break;
-    case 42: tile_go<4, 2>(t, p.tiles, stream); break;
-    case 22: tile_go<2, 2>(t, p.tiles, stream); break;
+  switch (kShapes[p.shape].code) {
+    case 44: tile_go<4, 2, 2, 4>(t, p.tiles, stream); break;
+    case 34: tile_go<3, 2, 2, 4>(t, p.tiles, stream); break;
+    case 43: tile_go<2, 3, 4, 2>(t, p.tiles, stream); break;
+    case 42: tile_go<2, 2, 4, 2>(t, p.tiles, stream); break;
+    case 22: tile_go<2, 2, 2, 2>(t, p.tiles, stream); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();

@@ -3,9 +3,11 @@ the gated residual norms and the rotary positions with several axes.
 
 Like the rest of the binding this module only checks and marshals arguments
 and allocates outputs; the arithmetic is in the library (include/svdq.h).  A call
-runs on the current device's current stream, or on ``stream``; tensors of
-another device are refused.  A block's pass, with the modulation vectors from
-``awq_w4a16_gemm``::
+runs on the current device's current stream, or on ``stream``: its outputs then
+belong to that stream, and inputs freed meanwhile are kept for it; ordering the
+two streams is the caller's part.  Tensors of another device are refused.
+
+A block's pass, with the modulation vectors from ``awq_w4a16_gemm``::
 
     h, (q, s) = gate_norm_modulate(x, y, gate=gate, scale=scale, shift=shift, quantize="int8")
     qkv = w8a8_gemm(q, s, w_codes, w_scales, bias)
@@ -25,6 +27,7 @@ _EPILOGUES = {"none": 0, "gelu_tanh": 1}
 _SPECTRA = {"axis": 0, "shared": 1}
 _LAYOUTS = {"pairs": 0, "halves": 1}
 _BF16 = torch.bfloat16
+_WS_COUNTERS = 1 << 20  # bytes of a workspace's arrival counters
 
 
 def _choice(table, value, name):
@@ -35,69 +38,116 @@ def _choice(table, value, name):
 
 
 def _device(t, stream, name):
-    """The device of a call's first tensor: the stream's, or the current one."""
-    dev = t.device
-    if t.numel() and dev.type != "cuda":
-        raise ValueError(f"{name}: must be a device tensor")
-    if dev.type == "cuda":
-        here = torch.cuda.current_device()
-        if dev.index != here or (stream is not None and stream.device_index != here):
-            raise ValueError(f"{name}: the tensors, the stream and the current device (cuda:{here}) must agree")
-    return dev
+    """The device index of a call's first tensor, which is the current device and the
+    stream's (-1: an empty host tensor)."""
+    idx = t.get_device()
+    if idx < 0:
+        if t.numel():
+            raise ValueError(f"{name}: must be a device tensor")
+        return idx
+    here = torch.cuda.current_device()
+    if idx != here or (stream is not None and stream.device_index != here):
+        raise ValueError(f"{name}: the tensors, the stream and the current device (cuda:{here}) must agree")
+    return idx
 
 
-def _raw_stream(dev, stream):
+def _current_stream(idx):
+    return torch.cuda.current_stream(idx).cuda_stream
+
+
+# the handle of the current stream without a Stream object around it (2 us less
+# per call), where this torch has it
+_raw_current = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
+def _raw_stream(idx, stream):
     if stream is not None:
         return stream.cuda_stream
-    return torch.cuda.current_stream(dev).cuda_stream if dev.type == "cuda" else None
+    return _raw_current(idx) if idx >= 0 else None
 
 
-def _dense(t, dtype, shape, dev, name):
+def _new(like, dtype, stream, *shape):
+    """A contiguous tensor of this shape on the device of `like`, memory of `stream`."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _new(like, dtype, None, *shape)
+    n = len(shape)
+    strides = (1,) if n == 1 else (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
+
+
+def _hold(stream, *tensors):
+    """Memory of these tensors is not reused before what `stream` has been given is done."""
+    for t in tensors:
+        if t is not None and t.get_device() >= 0:
+            t.record_stream(stream)
+
+
+def _gemm_workspace(need, device, stream, given):
+    """As the other calls' workspaces, except under capture: there every call gets
+    memory of the graph's own, its arrival counters cleared by the graph, so that
+    graphs captured on one stream share nothing."""
+    from . import _workspace
+    if given is None and stream is not None:
+        with torch.cuda.stream(stream):
+            return _gemm_workspace(need, device, None, None)
+    if given is None and torch.cuda.is_current_stream_capturing():
+        ws = torch.empty((need,), dtype=torch.uint8, device=device)
+        ws[:_WS_COUNTERS].zero_()
+        return ws.data_ptr(), need
+    return _workspace(need, device, stream, given)
+
+
+def _refuse(t, dtype, shape, idx, name):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != idx:
+        raise ValueError(f"{name}: must be on the device of the others, got {t.device}")
+    raise ValueError(f"{name}: {'a row ' if len(shape) > 1 else ''}must be contiguous")
+
+
+def _dense(t, dtype, shape, idx, name):
     """A contiguous tensor of exactly this type, shape and device -> its address."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    if t.device != dev:
-        raise ValueError(f"{name}: must be on {dev}, got {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == idx and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dtype, shape, idx, name)
 
 
-def _rows(t, dtype, shape, dev, name):
+def _rows(t, dtype, shape, idx, name):
     """As _dense, but rows (dimension 0) may lie any distance apart -> (address, row stride)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name}: must be on {dev}, got {t.device}")
-    width = 1
-    strides = t.stride()
-    for d in range(len(shape) - 1, 0, -1):
-        if strides[d] != width and shape[d] != 1 and shape[0]:
-            raise ValueError(f"{name}: a row must be contiguous")
-        width *= shape[d]
-    return t.data_ptr(), strides[0] if shape[0] > 1 else width
+    if t.dtype is dtype and t.shape == shape and t.get_device() == idx:
+        strides = t.stride()
+        if shape[0] > 1 and t.is_contiguous():
+            return t.data_ptr(), strides[0]
+        width = 1
+        for d in range(len(shape) - 1, 0, -1):
+            if strides[d] != width and shape[d] != 1:
+                break
+            width *= shape[d]
+        else:
+            return t.data_ptr(), strides[0] if shape[0] > 1 else width
+    _refuse(t, dtype, shape, idx, name)
 
 
 def quantize_act_int8(x, smooth=None, out=None, stream=None):
     """Per-token 8-bit quantization: x bf16 [M, K], smooth fp32 [K] or None (x is
     divided by it) -> (act_codes int8 [M, K], act_scales fp32 [M])."""
     M, K = x.shape
-    dev = _device(x, stream, "x")
-    px = _dense(x, _BF16, (M, K), dev, "x")
-    ps = None if smooth is None else _dense(smooth, torch.float32, (K,), dev, "smooth")
+    idx = _device(x, stream, "x")
+    px = _dense(x, _BF16, (M, K), idx, "x")
+    ps = None if smooth is None else _dense(smooth, torch.float32, (K,), idx, "smooth")
     if out is None:
-        codes = torch.empty((M, K), dtype=torch.int8, device=dev)
-        scales = torch.empty((M,), dtype=torch.float32, device=dev)
+        codes, scales = _new(x, torch.int8, stream, M, K), _new(x, torch.float32, stream, M)
         pc, pa = codes.data_ptr(), scales.data_ptr()
     else:
         codes, scales = out
-        pc = _dense(codes, torch.int8, (M, K), dev, "act_codes")
-        pa = _dense(scales, torch.float32, (M,), dev, "act_scales")
-    check(lib().svdq_quantize_act_int8(px, ps, M, K, pc, pa, _raw_stream(dev, stream)), "svdq_quantize_act_int8")
+        pc = _dense(codes, torch.int8, (M, K), idx, "act_codes")
+        pa = _dense(scales, torch.float32, (M,), idx, "act_scales")
+    check(lib().svdq_quantize_act_int8(px, ps, M, K, pc, pa, _raw_stream(idx, stream)), "svdq_quantize_act_int8")
+    if stream is not None:
+        _hold(stream, x, smooth)
     return codes, scales
 
 
@@ -108,26 +158,28 @@ def w8a8_gemm(act_codes, act_scales, w_codes, w_scales, bias=None, out=None, str
 
     epilogue "gelu_tanh" applies GELU (tanh form) to y + b before the rounding.
     """
-    from . import _workspace
     M, K = act_codes.shape
     N = w_codes.shape[0]
-    dev = _device(act_codes, stream, "act_codes")
-    pa = _dense(act_codes, torch.int8, (M, K), dev, "act_codes")
-    ps = _dense(act_scales, torch.float32, (M,), dev, "act_scales")
-    pw = _dense(w_codes, torch.int8, (N, K), dev, "w_codes")
-    pz = _dense(w_scales, torch.float32, (N,), dev, "w_scales")
-    pb = None if bias is None else _dense(bias, _BF16, (N,), dev, "bias")
+    idx = _device(act_codes, stream, "act_codes")
+    pa = _dense(act_codes, torch.int8, (M, K), idx, "act_codes")
+    ps = _dense(act_scales, torch.float32, (M,), idx, "act_scales")
+    pw = _dense(w_codes, torch.int8, (N, K), idx, "w_codes")
+    pz = _dense(w_scales, torch.float32, (N,), idx, "w_scales")
+    pb = None if bias is None else _dense(bias, _BF16, (N,), idx, "bias")
     epi = _choice(_EPILOGUES, epilogue, "epilogue")
     if out is None:
-        y = torch.empty((M, N), dtype=_BF16, device=dev)
+        y = _new(act_codes, _BF16, stream, M, N)
         py = y.data_ptr()
     else:
         y = out
-        py = _dense(y, _BF16, (M, N), dev, "y")
+        py = _dense(y, _BF16, (M, N), idx, "y")
     L = lib()
     need = L.svdq_w8a8_gemm_workspace_size(M, N, K)
-    ws, wsb = (None, 0) if need == 0 and workspace is None else _workspace(need, dev, stream, workspace)
-    check(L.svdq_w8a8_gemm(pa, ps, pw, pz, pb, M, N, K, epi, py, ws, wsb, _raw_stream(dev, stream)), "svdq_w8a8_gemm")
+    ws, wsb = (None, 0) if need == 0 and workspace is None else _gemm_workspace(
+        need, act_codes.device, stream, workspace)
+    check(L.svdq_w8a8_gemm(pa, ps, pw, pz, pb, M, N, K, epi, py, ws, wsb, _raw_stream(idx, stream)), "svdq_w8a8_gemm")
+    if stream is not None:
+        _hold(stream, act_codes, act_scales, w_codes, w_scales, bias)
     return y
 
 
@@ -155,9 +207,9 @@ def gate_norm_modulate(x, y=None, post_norm="none", post_weight=None, gate=None,
     [M, C], or (int8 [M, C], fp32 [M]), or None for norm="none".
     """
     M, C = x.shape
-    dev = _device(x, stream, "x")
+    idx = _device(x, stream, "x")
     fp32 = x.dtype is torch.float32
-    px, xs = _rows(x, torch.float32 if fp32 else _BF16, (M, C), dev, "x")
+    px, xs = _rows(x, torch.float32 if fp32 else _BF16, (M, C), idx, "x")
     post, kind = _choice(_NORMS, post_norm, "post_norm"), _choice(_NORMS, norm, "norm")
     if quantize not in (None, "int8"):
         raise ValueError(f"quantize: expected None or 'int8', got {quantize!r}")
@@ -165,48 +217,53 @@ def gate_norm_modulate(x, y=None, post_norm="none", post_weight=None, gate=None,
     ys = hs = gr = gs = mr = ms = 0
     h = z = None
     if y is not None:
-        py, ys = _rows(y, _BF16, (M, C), dev, "y")
-        h = torch.empty((M, C), dtype=x.dtype, device=dev) if h_out is None else h_out
-        ph, hs = _rows(h, x.dtype, (M, C), dev, "h")
+        py, ys = _rows(y, _BF16, (M, C), idx, "y")
+        if h_out is None:
+            h = _new(x, x.dtype, stream, M, C)
+            ph, hs = h.data_ptr(), C
+        else:
+            h = h_out
+            ph, hs = _rows(h, x.dtype, (M, C), idx, "h")
     elif h_out is not None:
         raise ValueError("h_out: there is no h without y")
     if post_weight is not None:
-        ppw = _dense(post_weight, _BF16, (C,), dev, "post_weight")
+        ppw = _dense(post_weight, _BF16, (C,), idx, "post_weight")
     if gate is not None:
         gr = gate.shape[0]
-        pg, gs = _rows(gate, _BF16, (gr, C), dev, "gate")
+        pg, gs = _rows(gate, _BF16, (gr, C), idx, "gate")
     if weight is not None:
-        pw = _dense(weight, _BF16, (C,), dev, "weight")
+        pw = _dense(weight, _BF16, (C,), idx, "weight")
     if scale is not None:
         mr = scale.shape[0]
-        psc, ms = _rows(scale, _BF16, (mr, C), dev, "scale")
+        psc, ms = _rows(scale, _BF16, (mr, C), idx, "scale")
     if shift is not None:
         if scale is None:
             mr = shift.shape[0]
-        psh, shs = _rows(shift, _BF16, (mr, C), dev, "shift")
+        psh, shs = _rows(shift, _BF16, (mr, C), idx, "shift")
         if scale is not None and shs != ms:
             raise ValueError("scale and shift: the row strides differ")
         ms = shs
     if smooth is not None:
-        psm = _dense(smooth, torch.float32, (C,), dev, "smooth")
+        psm = _dense(smooth, torch.float32, (C,), idx, "smooth")
     if kind:
         if quantize is None:
-            z = torch.empty((M, C), dtype=_BF16, device=dev) if out is None else out
-            pz = z.data_ptr() if out is None else _dense(z, _BF16, (M, C), dev, "z")
+            z = _new(x, _BF16, stream, M, C) if out is None else out
+            pz = z.data_ptr() if out is None else _dense(z, _BF16, (M, C), idx, "z")
         else:
             if out is None:
-                z = (torch.empty((M, C), dtype=torch.int8, device=dev),
-                     torch.empty((M,), dtype=torch.float32, device=dev))
+                z = _new(x, torch.int8, stream, M, C), _new(x, torch.float32, stream, M)
                 pz, pzs = z[0].data_ptr(), z[1].data_ptr()
             else:
                 z = (out[0], out[1])
-                pz = _dense(z[0], torch.int8, (M, C), dev, "z codes")
-                pzs = _dense(z[1], torch.float32, (M,), dev, "z scales")
+                pz = _dense(z[0], torch.int8, (M, C), idx, "z codes")
+                pzs = _dense(z[1], torch.float32, (M,), idx, "z scales")
     elif out is not None:
         raise ValueError("out: there is no z with norm='none'")
     check(lib().svdq_gate_norm_modulate(
         px, int(fp32), xs, py, ys, post, ppw, pg, gr, gs, residual_scale, kind, pw, psc, psh, mr, ms, eps, M, C,
-        ph, hs, int(quantize is not None), psm, pz, pzs, _raw_stream(dev, stream)), "svdq_gate_norm_modulate")
+        ph, hs, int(quantize is not None), psm, pz, pzs, _raw_stream(idx, stream)), "svdq_gate_norm_modulate")
+    if stream is not None:
+        _hold(stream, x, y, post_weight, gate, weight, scale, shift, smooth)
     return h, z
 
 
@@ -214,7 +271,7 @@ def _axes_array(axes):
     return (ctypes.c_int64 * len(axes))(*axes)
 
 
-def _positions(t, dev, n_axes):
+def _positions(t, idx, n_axes):
     """positions fp32 or int32 [P, n_axes] -> (address, type code, P)."""
     if t.dtype is torch.float32:
         code = 0
@@ -223,7 +280,7 @@ def _positions(t, dev, n_axes):
     else:
         raise TypeError(f"positions: expected torch.float32 or torch.int32, got {t.dtype}")
     P = t.shape[0]
-    return _dense(t, t.dtype, (P, n_axes), dev, "positions"), code, P
+    return _dense(t, t.dtype, (P, n_axes), idx, "positions"), code, P
 
 
 def rope_axes_tables(positions, axes, theta=10000.0, spectrum="axis", out=None, stream=None):
@@ -233,18 +290,20 @@ def rope_axes_tables(positions, axes, theta=10000.0, spectrum="axis", out=None, 
     axes: channels each axis turns.  spectrum "axis": each axis's rates fall from 1
     to about 1/theta over its own width; "shared": one series over all R channels,
     of which each axis owns a section."""
-    dev = _device(positions, stream, "positions")
-    pp, code, M = _positions(positions, dev, len(axes))
+    idx = _device(positions, stream, "positions")
+    pp, code, M = _positions(positions, idx, len(axes))
     half = sum(axes) // 2
     if out is None:
-        cos, sin = (torch.empty((M, half), dtype=torch.float32, device=dev) for _ in range(2))
+        cos, sin = (_new(positions, torch.float32, stream, M, half) for _ in range(2))
     else:
         cos, sin = out
-    pc = _dense(cos, torch.float32, (M, half), dev, "cos")
-    ps = _dense(sin, torch.float32, (M, half), dev, "sin")
+        _dense(cos, torch.float32, (M, half), idx, "cos")
+        _dense(sin, torch.float32, (M, half), idx, "sin")
     check(lib().svdq_rope_axes_tables(pp, code, M, len(axes), _axes_array(axes), theta,
-                                      _choice(_SPECTRA, spectrum, "spectrum"), pc, ps, _raw_stream(dev, stream)),
-          "svdq_rope_axes_tables")
+                                      _choice(_SPECTRA, spectrum, "spectrum"), cos.data_ptr(), sin.data_ptr(),
+                                      _raw_stream(idx, stream)), "svdq_rope_axes_tables")
+    if stream is not None:
+        _hold(stream, positions)
     return cos, sin
 
 
@@ -257,30 +316,35 @@ def rope_axes(q, k, positions, axes, theta=10000.0, spectrum="axis", layout="pai
     rope_axes_tables; layout "pairs" turns channels (2i, 2i+1), "halves" (i, i + R/2).
     Returns (q_out, k_out)."""
     M, Hq, D = q.shape
-    dev = _device(q, stream, "q")
-    pq, qs = _rows(q, _BF16, (M, Hq, D), dev, "q")
+    idx = _device(q, stream, "q")
+    pq, qs = _rows(q, _BF16, (M, Hq, D), idx, "q")
     pk = pko = None
     Hk = ks = kos = 0
     if k is not None:
         Hk = k.shape[1]
-        pk, ks = _rows(k, _BF16, (M, Hk, D), dev, "k")
+        pk, ks = _rows(k, _BF16, (M, Hk, D), idx, "k")
     if out is None:
-        qo = torch.empty((M, Hq, D), dtype=_BF16, device=dev)
-        ko = None if k is None else torch.empty((M, Hk, D), dtype=_BF16, device=dev)
+        qo = _new(q, _BF16, stream, M, Hq, D)
+        pqo, qos, ko = qo.data_ptr(), Hq * D, None
+        if k is not None:
+            ko = _new(q, _BF16, stream, M, Hk, D)
+            pko, kos = ko.data_ptr(), Hk * D
     else:
         qo, ko = out
         if (ko is None) != (k is None):
             raise ValueError("out: one output for q and one for k")
-    pqo, qos = _rows(qo, _BF16, (M, Hq, D), dev, "q_out")
-    if k is not None:
-        pko, kos = _rows(ko, _BF16, (M, Hk, D), dev, "k_out")
-    pp, code, P = _positions(positions, dev, len(axes))
-    pqn = None if q_norm is None else _dense(q_norm, _BF16, (D,), dev, "q_norm")
-    pkn = None if k_norm is None else _dense(k_norm, _BF16, (D,), dev, "k_norm")
+        pqo, qos = _rows(qo, _BF16, (M, Hq, D), idx, "q_out")
+        if k is not None:
+            pko, kos = _rows(ko, _BF16, (M, Hk, D), idx, "k_out")
+    pp, code, P = _positions(positions, idx, len(axes))
+    pqn = None if q_norm is None else _dense(q_norm, _BF16, (D,), idx, "q_norm")
+    pkn = None if k_norm is None else _dense(k_norm, _BF16, (D,), idx, "k_norm")
     check(lib().svdq_rope_axes(
         pq, qs, Hq, pk, ks, Hk, D, M, pp, code, P, len(axes), _axes_array(axes), theta,
         _choice(_SPECTRA, spectrum, "spectrum"), _choice(_LAYOUTS, layout, "layout"), pqn, pkn, eps, pqo, qos, pko,
-        kos, _raw_stream(dev, stream)), "svdq_rope_axes")
+        kos, _raw_stream(idx, stream)), "svdq_rope_axes")
+    if stream is not None:
+        _hold(stream, q, k, positions, q_norm, k_norm)
     return qo, ko
 
 

@@ -109,7 +109,7 @@ svdq_status svdq_quantize_act_int8(const void* x, const float* smooth, int64_t M
   if (s != SVDQ_STATUS_SUCCESS) return s;
   s = check_current_device();
   if (s != SVDQ_STATUS_SUCCESS) return s;
-  const svdq::QuantInt8Args a{static_cast<const uint16_t*>(x), smooth, act_codes, act_scales, (int)M, (int)K};
+  const svdq::QuantInt8Args a{static_cast<const uint16_t*>(x), smooth, act_codes, act_scales, (int)M, (int)K, 0};
   return launched(svdq::launch_quant_int8(a, static_cast<hipStream_t>(stream)), "quantize int8");
 }
 

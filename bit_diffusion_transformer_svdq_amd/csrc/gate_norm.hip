@@ -15,7 +15,12 @@
 //
 // Bound by HBM: every element of x and y is read once and of h and z written
 // once.  A row stays in registers between its reductions (mean, then centered
-// squares: no cancellation), W waves per row, V vectors of 8 channels per lane.
+// squares: no cancellation), W waves per row and V vectors of 8 channels per lane.
+// One row per workgroup (with W = 1: per wave) measured fastest: runs of rows with
+// the shared vectors in registers and the next row in flight lost more to
+// occupancy than they saved (4608 x 3072: 23.6-26 us against 22.7).  Only with a
+// smoothing vector, whose reciprocals are the dearest part, a workgroup takes a
+// run of rows and keeps the reciprocals (quantizer 4608 x 3072: 16.2 -> 11.2 us).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -30,20 +35,55 @@ constexpr int kWgWaves1 = 4;  // rows (waves) per workgroup when one wave owns a
 template <int W>
 constexpr int threads_of() { return W == 1 ? 64 * kWgWaves1 : 64 * W; }
 
-// the row this wave works on (uniform)
+// the first row of this workgroup's (W == 1: wave's) run of `run` rows
 template <int W>
-__device__ __forceinline__ int row_of() {
-  return W == 1 ? (int)blockIdx.x * kWgWaves1 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : (int)blockIdx.x;
+__device__ __forceinline__ int first_row(int run) {
+  const int owner = W == 1 ? (int)blockIdx.x * kWgWaves1 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)
+                           : (int)blockIdx.x;
+  return owner * run;  // below 2^25
 }
+
+__device__ __forceinline__ uint4 load8(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
+__device__ __forceinline__ void load_f8(const float* p, float (&f)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+}
+
+// 8 elements of the residual stream, as loaded
+template <bool F32>
+struct Stream8 {
+  uint4 lo, hi;
+  __device__ __forceinline__ void load(const void* x, size_t at) {
+    if constexpr (F32) {
+      const float* p = static_cast<const float*>(x) + at;
+      lo = *reinterpret_cast<const uint4*>(p);
+      hi = *reinterpret_cast<const uint4*>(p + 4);
+    } else {
+      lo = load8(static_cast<const uint16_t*>(x) + at);
+    }
+  }
+  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+    if constexpr (F32) {
+      f[0] = __builtin_bit_cast(float, lo.x), f[1] = __builtin_bit_cast(float, lo.y);
+      f[2] = __builtin_bit_cast(float, lo.z), f[3] = __builtin_bit_cast(float, lo.w);
+      f[4] = __builtin_bit_cast(float, hi.x), f[5] = __builtin_bit_cast(float, hi.y);
+      f[6] = __builtin_bit_cast(float, hi.z), f[7] = __builtin_bit_cast(float, hi.w);
+    } else {
+      unpack8(lo, f);
+    }
+  }
+};
 
 template <int W, int V, bool F32, bool Q8>
 __global__ __launch_bounds__(threads_of<W>()) void gate_norm_kernel(const GateNormArgs a) {
-  __shared__ float red[W > 1 ? 5 * W : 1];
-  const int row = row_of<W>();
-  if (row >= a.M) return;  // W == 1 only: no barrier follows
+  __shared__ float red_all[W > 1 ? 10 * W : 1];  // two sets of reduction slots, rows take turns
+  const int row0 = first_row<W>(a.run), row_end = min(row0 + a.run, a.M);
+  if (row0 >= row_end) return;
   const int lane0 = W == 1 ? (threadIdx.x & 63) : threadIdx.x;
   const int C8 = a.C >> 3;
   const float inv_c = 1.0f / (float)a.C;
+  const bool has_y = a.y != nullptr, has_z = a.norm != kNormNone;
 
   // vector v of a lane: channels 8 i .. 8 i + 7, i = v * 64 W + lane; only the
   // last vector can lie past the row, its loads then repeat the last one
@@ -52,165 +92,185 @@ __global__ __launch_bounds__(threads_of<W>()) void gate_norm_kernel(const GateNo
   for (int v = 0; v < V; ++v) off[v] = 8 * min(v * 64 * W + lane0, C8 - 1);
   const bool live = (V - 1) * 64 * W + lane0 < C8;
 
-  float h[V][8];
-  if constexpr (F32) {
-    const float* x = static_cast<const float*>(a.x) + (size_t)row * a.x_stride;
+  // the reciprocals stay in registers over a run, except where a row alone
+  // fills them (16 waves, more than 8192 channels)
+  constexpr bool kKeep = Q8 && (W < 16 || V == 1);
+  float mu[kKeep ? V : 1][8];
+  auto reciprocals = [&](int v, float (&m)[8]) {
+    float sm[8];
+    load_f8(a.smooth + off[v], sm);
+    recip8(sm, m);
+  };
+  if constexpr (kKeep) {
+    if (a.smooth != nullptr) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) reciprocals(v, mu[v]);
+    }
+  }
+  Stream8<F32> px[V];
+  uint4 py[V];
+  auto fetch = [&](int row) {
+    const size_t xo = (size_t)row * a.x_stride, yo = (size_t)row * a.y_stride;
+#pragma unroll
+    for (int v = 0; v < V; ++v) px[v].load(a.x, xo + off[v]);
+    if (has_y) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) py[v] = load8(a.y + yo + off[v]);
+    }
+  };
+
+
+  for (int row = row0; row < row_end; ++row) {
+    float* red = red_all + (W > 1 ? 5 * W * (row & 1) : 0);
+    fetch(row);
+    const uint16_t* gate = a.gate + (size_t)(row / a.gate_every) * a.gate_stride;
+    const size_t mod = (size_t)(row / a.mod_every) * a.mod_stride;
+    float h[V][8], u[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const float4 p = *reinterpret_cast<const float4*>(x + off[v]);
-      const float4 q = *reinterpret_cast<const float4*>(x + off[v] + 4);
-      h[v][0] = p.x, h[v][1] = p.y, h[v][2] = p.z, h[v][3] = p.w;
-      h[v][4] = q.x, h[v][5] = q.y, h[v][6] = q.z, h[v][7] = q.w;
+      px[v].unpack(h[v]);
+      if (has_y) unpack8(py[v], u[v]);
     }
-  } else {
-    const uint16_t* x = static_cast<const uint16_t*>(a.x) + (size_t)row * a.x_stride;
-#pragma unroll
-    for (int v = 0; v < V; ++v) unpack8(*reinterpret_cast<const uint4*>(x + off[v]), h[v]);
-  }
 
-  if (a.y != nullptr) {
-    const uint16_t* y = a.y + (size_t)row * a.y_stride;
-    float u[V][8];
+    if (has_y) {
+      if (a.post != kNormNone) {
+        float mean = 0.f;
+        if (a.post == kNormLayer) {
+          float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) unpack8(*reinterpret_cast<const uint4*>(y + off[v]), u[v]);
-    if (a.post != kNormNone) {
-      float mean = 0.f;
-      if (a.post == kNormLayer) {
-        float s = 0.f;
+          for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += (v < V - 1 || live) ? u[v][e] : 0.f;
+          mean = row_reduce<SumOp, W>(s, red, 0) * inv_c;
+        }
+        float ss = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s += (v < V - 1 || live) ? u[v][e] : 0.f;
-        mean = row_reduce<SumOp, W>(s, red, 0) * inv_c;
-      }
-      float ss = 0.f;
+          for (int e = 0; e < 8; ++e) {
+            u[v][e] -= mean;
+            ss = (v < V - 1 || live) ? __builtin_fmaf(u[v][e], u[v][e], ss) : ss;
+          }
+        const float r = 1.0f / sqrtf(__builtin_fmaf(row_reduce<SumOp, W>(ss, red, 1), inv_c, a.eps));
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+          if (a.post_weight != nullptr) {
+            float w[8];
+            unpack8(load8(a.post_weight + off[v]), w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          u[v][e] -= mean;
-          ss = (v < V - 1 || live) ? __builtin_fmaf(u[v][e], u[v][e], ss) : ss;
+            for (int e = 0; e < 8; ++e) u[v][e] *= r * w[e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[v][e] *= r;
+          }
         }
-      const float r = 1.0f / sqrtf(__builtin_fmaf(row_reduce<SumOp, W>(ss, red, 1), inv_c, a.eps));
+      }
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float w[8];
-        if (a.post_weight != nullptr) {
-          unpack8(*reinterpret_cast<const uint4*>(a.post_weight + off[v]), w);
+        if (a.gate != nullptr) {
+          float g[8];
+          unpack8(load8(gate + off[v]), g);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[v][e] *= r * w[e];
+          for (int e = 0; e < 8; ++e) h[v][e] = __builtin_fmaf(g[e], u[v][e], a.alpha * h[v][e]);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[v][e] *= r;
+          for (int e = 0; e < 8; ++e) h[v][e] = __builtin_fmaf(a.alpha, h[v][e], u[v][e]);
         }
       }
-    }
-    const uint16_t* gate = a.gate + (size_t)(row / a.gate_every) * a.gate_stride;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (a.gate != nullptr) {
-        float g[8];
-        unpack8(*reinterpret_cast<const uint4*>(gate + off[v]), g);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[v][e] = __builtin_fmaf(g[e], u[v][e], a.alpha * h[v][e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[v][e] = __builtin_fmaf(a.alpha, h[v][e], u[v][e]);
-      }
-    }
-    if constexpr (F32) {
-      float* ho = static_cast<float*>(a.h) + (size_t)row * a.h_stride;
+      const size_t ho = (size_t)row * a.h_stride;
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (v < V - 1 || live) {
-          *reinterpret_cast<float4*>(ho + off[v]) = float4{h[v][0], h[v][1], h[v][2], h[v][3]};
-          *reinterpret_cast<float4*>(ho + off[v] + 4) = float4{h[v][4], h[v][5], h[v][6], h[v][7]};
+          if constexpr (F32) {
+            float* p = static_cast<float*>(a.h) + ho + off[v];
+            *reinterpret_cast<float4*>(p) = float4{h[v][0], h[v][1], h[v][2], h[v][3]};
+            *reinterpret_cast<float4*>(p + 4) = float4{h[v][4], h[v][5], h[v][6], h[v][7]};
+          } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.h) + ho + off[v]) = pack8(h[v]);
+          }
         }
-    } else {
-      uint16_t* ho = static_cast<uint16_t*>(a.h) + (size_t)row * a.h_stride;
+    }
+    if (!has_z) continue;
+
+    float mean = 0.f;
+    if (a.norm == kNormLayer) {
+      float s = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (v < V - 1 || live) *reinterpret_cast<uint4*>(ho + off[v]) = pack8(h[v]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += (v < V - 1 || live) ? h[v][e] : 0.f;
+      mean = row_reduce<SumOp, W>(s, red, 2) * inv_c;
     }
-  }
-  if (a.norm == kNormNone) return;
-
-  float mean = 0.f;
-  if (a.norm == kNormLayer) {
-    float s = 0.f;
+    float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += (v < V - 1 || live) ? h[v][e] : 0.f;
-    mean = row_reduce<SumOp, W>(s, red, 2) * inv_c;
-  }
-  float ss = 0.f;
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      h[v][e] -= mean;
-      ss = (v < V - 1 || live) ? __builtin_fmaf(h[v][e], h[v][e], ss) : ss;
-    }
-  const float r = 1.0f / sqrtf(__builtin_fmaf(row_reduce<SumOp, W>(ss, red, 3), inv_c, a.eps));
-  const size_t mod = (size_t)(row / a.mod_every) * a.mod_stride;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[v][e] *= r;
-    float w[8];
-    if (a.weight != nullptr) {
-      unpack8(*reinterpret_cast<const uint4*>(a.weight + off[v]), w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[v][e] *= w[e];
-    }
-    if (a.scale != nullptr) {
-      unpack8(*reinterpret_cast<const uint4*>(a.scale + mod + off[v]), w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[v][e] = __builtin_fmaf(h[v][e], w[e], h[v][e]);
-    }
-    if (a.shift != nullptr) {
-      unpack8(*reinterpret_cast<const uint4*>(a.shift + mod + off[v]), w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[v][e] += w[e];
-    }
-  }
-  if constexpr (!Q8) {
-    uint16_t* z = static_cast<uint16_t*>(a.z) + (size_t)row * a.C;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v < V - 1 || live) *reinterpret_cast<uint4*>(z + off[v]) = pack8(h[v]);
-  } else {
-    float amax = 0.f;
+      for (int e = 0; e < 8; ++e) {
+        h[v][e] -= mean;
+        ss = (v < V - 1 || live) ? __builtin_fmaf(h[v][e], h[v][e], ss) : ss;
+      }
+    const float r = 1.0f / sqrtf(__builtin_fmaf(row_reduce<SumOp, W>(ss, red, 3), inv_c, a.eps));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (a.smooth != nullptr) {
-        float sm[8], mu[8];
-        const float4 p = *reinterpret_cast<const float4*>(a.smooth + off[v]);
-        const float4 q = *reinterpret_cast<const float4*>(a.smooth + off[v] + 4);
-        sm[0] = p.x, sm[1] = p.y, sm[2] = p.z, sm[3] = p.w, sm[4] = q.x, sm[5] = q.y, sm[6] = q.z, sm[7] = q.w;
-        recip8(sm, mu);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[v][e] *= mu[e];
+      for (int e = 0; e < 8; ++e) h[v][e] *= r;
+      float w[8];
+      if (a.weight != nullptr) {
+        unpack8(load8(a.weight + off[v]), w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[v][e] *= w[e];
       }
-      // (a lane past the row may hold what an update in place has already
-      // written there: it takes no part)
+      if (a.scale != nullptr) {
+        unpack8(load8(a.scale + mod + off[v]), w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        amax = (v < V - 1 || live) ? BitMaxOp::run(amax, __builtin_fabsf(h[v][e])) : amax;
+        for (int e = 0; e < 8; ++e) h[v][e] = __builtin_fmaf(h[v][e], w[e], h[v][e]);
+      }
+      if (a.shift != nullptr) {
+        unpack8(load8(a.shift + mod + off[v]), w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[v][e] += w[e];
+      }
     }
-    amax = row_reduce<BitMaxOp, W>(amax, red, 4);
-    float s, inv;
-    token_scale(amax, s, inv);
-    if (lane0 == 0) a.scales[row] = s;
-    int8_t* q = static_cast<int8_t*>(a.z) + (size_t)row * a.C;
+    const size_t zo = (size_t)row * a.C;
+    if constexpr (!Q8) {
+      uint16_t* z = static_cast<uint16_t*>(a.z) + zo;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v < V - 1 || live) {
-        row_v2u c = {codes4(&h[v][0], inv), codes4(&h[v][4], inv)};
-        if (inv == 0.f) c = row_v2u{0u, 0u};
-        *reinterpret_cast<row_v2u*>(q + off[v]) = c;
+      for (int v = 0; v < V; ++v)
+        if (v < V - 1 || live) *reinterpret_cast<uint4*>(z + off[v]) = pack8(h[v]);
+    } else {
+      float amax = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (a.smooth != nullptr) {
+          float m[8];
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m[e] = mu[v][e];
+          } else {
+            reciprocals(v, m);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[v][e] *= m[e];
+        }
+        // (a lane past the row may hold what an update in place has already
+        // written there: it takes no part)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          amax = (v < V - 1 || live) ? BitMaxOp::run(amax, __builtin_fabsf(h[v][e])) : amax;
       }
+      amax = row_reduce<BitMaxOp, W>(amax, red, 4);
+      float s, inv;
+      token_scale(amax, s, inv);
+      if (lane0 == 0) a.scales[row] = s;
+      int8_t* q = static_cast<int8_t*>(a.z) + zo;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v < V - 1 || live) {
+          row_v2u c = {codes4(&h[v][0], inv), codes4(&h[v][4], inv)};
+          if (inv == 0.f) c = row_v2u{0u, 0u};
+          *reinterpret_cast<row_v2u*>(q + off[v]) = c;
+        }
+    }
   }
 }
 
@@ -218,56 +278,76 @@ __global__ __launch_bounds__(threads_of<W>()) void gate_norm_kernel(const GateNo
 // q = rint(x_hat fl32(1/s)).  The row is kept as packed bf16.
 template <int W, int V, bool kSmooth>
 __global__ __launch_bounds__(threads_of<W>()) void quant_int8_kernel(const QuantInt8Args a) {
-  __shared__ float red[W > 1 ? W : 1];
-  const int row = row_of<W>();
-  if (row >= a.M) return;  // W == 1 only
+  constexpr bool kKeep = V <= 2;  // reciprocals stay in registers over the run of rows
+  __shared__ float red_all[W > 1 ? 2 * W : 1];
+  const int row0 = first_row<W>(a.run), row_end = min(row0 + a.run, a.M);
+  if (row0 >= row_end) return;
   const int lane0 = W == 1 ? (threadIdx.x & 63) : threadIdx.x;
   const int K8 = a.K >> 3;
   int off[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) off[v] = 8 * min(v * 64 * W + lane0, K8 - 1);
   const bool live = (V - 1) * 64 * W + lane0 < K8;
-  const uint16_t* x = a.x + (size_t)row * a.K;
-  uint4 p[V];
+  float mu[kKeep ? V : 1][8];
+  auto reciprocals = [&](int v, float (&m)[8]) {
+    float sm[8];
+    load_f8(a.smooth + off[v], sm);
+    recip8(sm, m);
+  };
+  if constexpr (kSmooth && kKeep) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) p[v] = *reinterpret_cast<const uint4*>(x + off[v]);
-  float amax = 0.f;
+    for (int v = 0; v < V; ++v) reciprocals(v, mu[v]);
+  }
+  for (int row = row0; row < row_end; ++row) {
+    uint4 p[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    float f[8];
-    unpack8(p[v], f);
-    if constexpr (kSmooth) {
-      float sm[8], mu[8];
-      const float4 s0 = *reinterpret_cast<const float4*>(a.smooth + off[v]);
-      const float4 s1 = *reinterpret_cast<const float4*>(a.smooth + off[v] + 4);
-      sm[0] = s0.x, sm[1] = s0.y, sm[2] = s0.z, sm[3] = s0.w, sm[4] = s1.x, sm[5] = s1.y, sm[6] = s1.z, sm[7] = s1.w;
-      recip8(sm, mu);
+    for (int v = 0; v < V; ++v) p[v] = load8(a.x + (size_t)row * a.K + off[v]);
+    float amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] *= mu[e];
-      p[v] = pack8(f);
+    for (int v = 0; v < V; ++v) {
+      float f[8];
       unpack8(p[v], f);
+      if constexpr (kSmooth) {
+        float m[8];
+        if constexpr (kKeep) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m[e] = mu[v][e];
+        } else {
+          reciprocals(v, m);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= m[e];
+        p[v] = pack8(f);
+        unpack8(p[v], f);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = BitMaxOp::run(amax, __builtin_fabsf(f[e]));
     }
+    amax = row_reduce<BitMaxOp, W>(amax, red_all + (W > 1 ? W * (row & 1) : 0), 0);
+    float s, inv;
+    token_scale(amax, s, inv);
+    if (lane0 == 0) a.scales[row] = s;
+    int8_t* q = a.codes + (size_t)row * a.K;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = BitMaxOp::run(amax, __builtin_fabsf(f[e]));
+    for (int v = 0; v < V; ++v) {
+      float f[8];
+      unpack8(p[v], f);
+      row_v2u c = {codes4(&f[0], inv), codes4(&f[4], inv)};
+      if (inv == 0.f) c = row_v2u{0u, 0u};
+      if (v < V - 1 || live) *reinterpret_cast<row_v2u*>(q + off[v]) = c;
+    }
   }
-  amax = row_reduce<BitMaxOp, W>(amax, red, 0);
-  float s, inv;
-  token_scale(amax, s, inv);
-  if (lane0 == 0) a.scales[row] = s;
-  int8_t* q = a.codes + (size_t)row * a.K;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    float f[8];
-    unpack8(p[v], f);
-    row_v2u c = {codes4(&f[0], inv), codes4(&f[4], inv)};
-    if (inv == 0.f) c = row_v2u{0u, 0u};
-    if (v < V - 1 || live) *reinterpret_cast<row_v2u*>(q + off[v]) = c;
-  }
+}
+
+template <int W>
+dim3 grid_of(int M, int run) {
+  const int owners = (M + run - 1) / run;
+  return dim3(W == 1 ? (owners + kWgWaves1 - 1) / kWgWaves1 : owners);
 }
 
 template <int W, int V>
 void gate_norm_go(const GateNormArgs& a, hipStream_t stream) {
-  const dim3 grid(W == 1 ? (a.M + kWgWaves1 - 1) / kWgWaves1 : a.M), block(threads_of<W>());
+  const dim3 grid = grid_of<W>(a.M, a.run), block(threads_of<W>());
   if (a.x_fp32) {
     if (a.scales) hipLaunchKernelGGL((gate_norm_kernel<W, V, true, true>), grid, block, 0, stream, a);
     else hipLaunchKernelGGL((gate_norm_kernel<W, V, true, false>), grid, block, 0, stream, a);
@@ -277,56 +357,100 @@ void gate_norm_go(const GateNormArgs& a, hipStream_t stream) {
   }
 }
 
-template <int W, int V>
+template <int W, int V, bool kSmooth>
 void quant_go(const QuantInt8Args& a, hipStream_t stream) {
-  const dim3 grid(W == 1 ? (a.M + kWgWaves1 - 1) / kWgWaves1 : a.M), block(threads_of<W>());
-  if (a.smooth) hipLaunchKernelGGL((quant_int8_kernel<W, V, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((quant_int8_kernel<W, V, false>), grid, block, 0, stream, a);
+  hipLaunchKernelGGL((quant_int8_kernel<W, V, kSmooth>), grid_of<W>(a.M, a.run), dim3(threads_of<W>()), 0, stream, a);
 }
+template <int W, int V>
+void quant_smooth(const QuantInt8Args& a, hipStream_t stream) { quant_go<W, V, true>(a, stream); }
+template <int W, int V>
+void quant_plain(const QuantInt8Args& a, hipStream_t stream) { quant_go<W, V, false>(a, stream); }
 
-// waves per row: one while the row fits its registers and there are rows
-// enough to occupy every SIMD, else as many as keep the row in registers
-int waves_for(int64_t M, int c8) {
-  if (c8 <= 512 && M >= 2 * 4 * (int64_t)current_cus()) return 1;
-  if (c8 <= 1024) return 4;
-  return c8 <= 2048 ? 8 : 16;
+// Waves per row: the fewest that leave a lane at most `per_lane` vectors, up to 16.
+// With no more rows than compute units a row's latency counts and a lane takes
+// one vector.
+int waves_for(int64_t M, int c8, int per_lane) {
+  if (M <= current_cus()) per_lane = 1;
+  int w = 1;
+  while (w < 16 && c8 > 64 * per_lane * w) w *= 2;
+  return w;
+}
+// Measured on MI355X (us, W waves and V vectors; the best of each marked *):
+//  gate norm  4608 x 1536: W1V3 15.0, W2V2 14.7, W4V1 13.8*    4608 x 5120: W4V3 41.1*, W8V2 46.4
+//             4608 x 3072: W2V3 24.7, W4V2 24.5, W8V1 24.2*    4608 x 4096: W2V4 36.5, W4V2 31.4, W8V1 31.2*
+//             8346 x 2304 fp32: W2V3 49.8*, W4V2 50.8          2304 x 8192: W4V4 35.1, W8V2 33.3*
+//  quantizer  4608 x 3072: W1V6 8.6*, W4V2 9.1, W8V1 10.1;  smoothed: W1V6 16.0, W2V3 13.8, W4V2 11.2*
+//             4608 x 12288: W4V6 29.2, W8V3 28.2*, W16V2 30.8;  smoothed: W4V6 49.5, W16V2 35.7*
+constexpr int kNormPerLane = 3, kQuantPerLane = 8, kQuantSmoothPerLane = 2;
+
+// Rows per run: one, or with a smoothing vector as many as leave kWavesPerCu
+// waves per compute unit.
+constexpr int kWavesPerCu = 32;
+int run_for(int64_t M, int w, bool smooth) {
+  if (!smooth) return 1;
+  const int64_t owners = (int64_t)current_cus() * kWavesPerCu / w;
+  return (int)((M + owners - 1) / owners);
 }
 
 }  // namespace
 
-hipError_t launch_gate_norm(const GateNormArgs& a, hipStream_t stream) {
-  const int c8 = a.C >> 3;
-  const int w = waves_for(a.M, c8);
-  const int v = (c8 + 64 * w - 1) / (64 * w);
-#define SVDQ_CASE(W, V) \
-  case 16 * W + V: gate_norm_go<W, V>(a, stream); break;
+#define SVDQ_AT(go, W, V) \
+  case 16 * W + V: go<W, V>(a, stream); break;
+#define SVDQ_TO2(go, W) SVDQ_AT(go, W, 1) SVDQ_AT(go, W, 2)
+#define SVDQ_TO3(go, W) SVDQ_TO2(go, W) SVDQ_AT(go, W, 3)
+#define SVDQ_5TO8(go, W) SVDQ_AT(go, W, 5) SVDQ_AT(go, W, 6) SVDQ_AT(go, W, 7) SVDQ_AT(go, W, 8)
+#define SVDQ_TO8(go, W) SVDQ_TO3(go, W) SVDQ_AT(go, W, 4) SVDQ_5TO8(go, W)
+
+hipError_t launch_gate_norm(const GateNormArgs& args, hipStream_t stream) {
+  GateNormArgs a = args;
+  const int c8 = a.C >> 3, w = waves_for(a.M, c8, kNormPerLane), v = (c8 + 64 * w - 1) / (64 * w);
+  a.run = run_for(a.M, w, a.smooth != nullptr);
   switch (16 * w + v) {
-    SVDQ_CASE(1, 1) SVDQ_CASE(1, 2) SVDQ_CASE(1, 3) SVDQ_CASE(1, 4)
-    SVDQ_CASE(1, 5) SVDQ_CASE(1, 6) SVDQ_CASE(1, 7) SVDQ_CASE(1, 8)
-    SVDQ_CASE(4, 1) SVDQ_CASE(4, 2) SVDQ_CASE(4, 3) SVDQ_CASE(4, 4)
-    SVDQ_CASE(8, 3) SVDQ_CASE(8, 4) SVDQ_CASE(16, 3) SVDQ_CASE(16, 4)
+    SVDQ_TO3(gate_norm_go, 1)
+    SVDQ_TO3(gate_norm_go, 2)
+    SVDQ_TO3(gate_norm_go, 4)
+    SVDQ_TO3(gate_norm_go, 8)
+    SVDQ_TO3(gate_norm_go, 16)
+    SVDQ_AT(gate_norm_go, 16, 4)
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
 }
 
-hipError_t launch_quant_int8(const QuantInt8Args& a, hipStream_t stream) {
-  const int k8 = a.K >> 3;
-  const int w = k8 > 2048 ? 16 : k8 > 1024 ? 4 : waves_for(a.M, k8);
+hipError_t launch_quant_int8(const QuantInt8Args& args, hipStream_t stream) {
+  QuantInt8Args a = args;
+  const bool smooth = a.smooth != nullptr;
+  const int k8 = a.K >> 3, w = waves_for(a.M, k8, smooth ? kQuantSmoothPerLane : kQuantPerLane);
   const int v = (k8 + 64 * w - 1) / (64 * w);
-#undef SVDQ_CASE
-#define SVDQ_CASE(W, V) \
-  case 16 * W + V: quant_go<W, V>(a, stream); break;
-  switch (16 * w + v) {
-    SVDQ_CASE(1, 1) SVDQ_CASE(1, 2) SVDQ_CASE(1, 3) SVDQ_CASE(1, 4)
-    SVDQ_CASE(1, 5) SVDQ_CASE(1, 6) SVDQ_CASE(1, 7) SVDQ_CASE(1, 8)
-    SVDQ_CASE(4, 1) SVDQ_CASE(4, 2) SVDQ_CASE(4, 3) SVDQ_CASE(4, 4)
-    SVDQ_CASE(4, 5) SVDQ_CASE(4, 6) SVDQ_CASE(4, 7) SVDQ_CASE(4, 8)
-    SVDQ_CASE(16, 3) SVDQ_CASE(16, 4) SVDQ_CASE(16, 5) SVDQ_CASE(16, 6) SVDQ_CASE(16, 7) SVDQ_CASE(16, 8)
-    default: return hipErrorInvalidValue;
+  a.run = run_for(a.M, w, smooth);
+  if (smooth) {
+    switch (16 * w + v) {
+      SVDQ_TO2(quant_smooth, 1)
+      SVDQ_TO2(quant_smooth, 2)
+      SVDQ_TO2(quant_smooth, 4)
+      SVDQ_TO2(quant_smooth, 8)
+      SVDQ_TO8(quant_smooth, 16)
+      default: return hipErrorInvalidValue;
+    }
+  } else {
+    switch (16 * w + v) {
+      SVDQ_TO8(quant_plain, 1)
+      SVDQ_AT(quant_plain, 2, 1)
+      SVDQ_5TO8(quant_plain, 2)
+      SVDQ_AT(quant_plain, 4, 1)
+      SVDQ_5TO8(quant_plain, 4)
+      SVDQ_AT(quant_plain, 8, 1)
+      SVDQ_5TO8(quant_plain, 8)
+      SVDQ_TO8(quant_plain, 16)
+      default: return hipErrorInvalidValue;
+    }
   }
-#undef SVDQ_CASE
   return hipGetLastError();
 }
+#undef SVDQ_AT
+#undef SVDQ_TO2
+#undef SVDQ_TO3
+#undef SVDQ_5TO8
+#undef SVDQ_TO8
 
 }  // namespace svdq

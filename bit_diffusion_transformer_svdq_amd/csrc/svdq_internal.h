@@ -174,6 +174,7 @@ struct GateNormArgs {
   int gate_every, mod_every;    // rows that share a gate row, a scale / shift row
   int post, norm, x_fp32;
   float alpha, eps;
+  int run;                      // rows per workgroup, set by the launcher
 };
 hipError_t launch_gate_norm(const GateNormArgs& a, hipStream_t stream);
 
@@ -185,6 +186,7 @@ struct QuantInt8Args {
   int8_t* codes;        // [M, K]
   float* scales;        // [M]
   int M, K;
+  int run;              // rows per workgroup, set by the launcher
 };
 hipError_t launch_quant_int8(const QuantInt8Args& a, hipStream_t stream);
 

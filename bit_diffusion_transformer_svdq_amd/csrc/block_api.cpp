@@ -119,8 +119,7 @@ size_t svdq_w8a8_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
 }
 
 svdq_status svdq_debug_set_w8a8_plan(int tile, int splits) {
-  if (tile != 0 && tile != 1 && tile != 22 && tile != 42 && tile != 43 && tile != 34 && tile != 44)
-    return fail(SVDQ_STATUS_INVALID_VALUE, "bad w8a8 tile %d (0, 1, 22, 42, 43, 34 or 44)", tile);
+  if (!svdq::w8a8_tile_known(tile)) return fail(SVDQ_STATUS_INVALID_VALUE, "unknown w8a8 tile %d", tile);
   if (splits < 0 || splits > 16) return fail(SVDQ_STATUS_INVALID_VALUE, "bad split count %d (0..16)", splits);
   svdq::set_w8a8_plan_override(tile, splits);
   return ok();

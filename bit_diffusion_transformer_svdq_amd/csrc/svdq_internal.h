@@ -203,8 +203,9 @@ struct W8a8Args {
 };
 size_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_w8a8_gemm(const W8a8Args& a, Workspace ws, hipStream_t stream);
-// Test hook: tile 0 by shape, 1 the few-token kernel where M <= 64, else 10 WI + WJ;
-// splits 0 by shape.
+// Test hook: tile 0 by shape, 1 the few-token kernel where M <= 16, else one of the
+// workgroup tiles; splits 0 by shape.
+bool w8a8_tile_known(int tile);
 void set_w8a8_plan_override(int tile, int splits);
 
 // Rotary positions with several axes (rope_axes.hip).

@@ -13,12 +13,12 @@
 //  * workgroup tile 64 WI weight rows x 64 WJ token rows, 4 waves as 2 x 2, each
 //    32 WI x 32 WJ = WI x WJ tiles of v_mfma_i32_32x32x32_i8 (WI = WJ = 4: 256
 //    int32 accumulators per lane, one wave per SIMD);
-//  * two LDS stages of 128 bytes per row, filled by global_load_lds_dwordx4 with
+//  * R LDS stages of 128 bytes per row, filled by global_load_lds_dwordx4 with
 //    8 whole 128-byte row runs per instruction.  A stage is computed in two
 //    halves: while the MFMAs of the first run, the fragments of the second are
-//    read; after that the stage's LDS is free, its DMA for stage q + 2 is
+//    read; after that the stage's LDS is free, its DMA for stage q + R is
 //    issued, and while the second half's MFMAs run the first half of stage
-//    q + 1 is read.  One barrier per stage, with a whole stage of MFMAs between
+//    q + 1 is read.  One barrier per stage, with R - 1 stages of MFMAs between
 //    a DMA and the wait for it;
 //  * 16-byte granule g of row R sits at slot 8 R + (g ^ R[3:1]).  A 16-byte LDS
 //    read runs in phases of 16 lanes (0-3, 12-15, 20-23, 24-27; 4-11, 16-19, 28-31;
@@ -36,6 +36,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "row_device.h"
@@ -99,30 +100,28 @@ struct TileArgs {
   int* part;     // int32 partials [sub-tile][splits][WI WJ 16][64]
 };
 
-// GELU (tanh form) as x - x / (exp(2u) + 1) with exp(2u) = 2^(x (c0 + c1 x^2)): one
-// exponential and one reciprocal, five other operations; within 2^-21 |x|
-__device__ __forceinline__ float gelu_exp2(float x) {
-  constexpr float c0 = 2.302208198f, c1 = 0.1029432397f;  // 2 sqrt(2/pi) log2(e), and 0.044715 times it
-  const float e = __builtin_amdgcn_exp2f(x * __builtin_fmaf(c1, x * x, c0));
-  return __builtin_fmaf(-x, __builtin_amdgcn_rcpf(e + 1.0f), x);
-}
-
-// WN x WM waves of WI x WJ tiles of 32 x 32
-template <int WI, int WJ, int WN, int WM>
+// WN x WM waves of WI x WJ tiles of 32 x 32, R stages in LDS
+template <int WI, int WJ, int WN, int WM, int R>
 struct Shape {
   static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves;
   static constexpr int kTN = 32 * WI * WN, kTM = 32 * WJ * WM;
-  static constexpr int kWgs = 2 * 128 * (kTN + kTM) > 80 * 1024 ? 1 : 2;  // per CU, by LDS
+  static constexpr int kLds = R * 128 * (kTN + kTM);
+  static constexpr int kWgs = kLds > 80 * 1024 ? 1 : 2;  // per CU, by LDS
   static constexpr int kSub = WI * WJ * 1024;                             // accumulators of a wave
 };
 
-template <int WI, int WJ, int WN, int WM, bool kSplit>
-__global__ __launch_bounds__((Shape<WI, WJ, WN, WM>::kThreads), 2) void w8a8_tile_kernel(const TileArgs p) {
-  using Sh = Shape<WI, WJ, WN, WM>;
+template <int WI, int WJ, int WN, int WM, int R, bool kSplit>
+__global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_tile_kernel(const TileArgs p) {
+  using Sh = Shape<WI, WJ, WN, WM, R>;
+  static_assert(R >= 2 && R <= 4, "stage buffers");
   constexpr int kTN = Sh::kTN, kTM = Sh::kTM, kWaves = Sh::kWaves;
   // one LDS object per operand and stage, so the compiler sees that a DMA
   // into one cannot alias reads of another
   __shared__ __attribute__((aligned(16))) uint8_t w0[kTN * 128], w1[kTN * 128], a0[kTM * 128], a1[kTM * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t w2[R > 2 ? kTN * 128 : 16], a2[R > 2 ? kTM * 128 : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t w3[R > 3 ? kTN * 128 : 16], a3[R > 3 ? kTM * 128 : 16];
+  auto wbuf = [&](int b) -> uint8_t* { return b == 0 ? w0 : b == 1 ? w1 : b == 2 ? w2 : w3; };
+  auto abuf = [&](int b) -> uint8_t* { return b == 0 ? a0 : b == 1 ? a1 : b == 2 ? a2 : a3; };
 
   const int M = p.g.M, N = p.g.N, K = p.g.K;
   int tm, tn;
@@ -170,9 +169,9 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM>::kThreads), 2) void w8a8_til
   auto dma_one = [&](int k, u32 col, auto bc) {
     constexpr int b = decltype(bc)::value;
     if (k < kWd)
-      dma16(wbase + (woff[k] + col), (b ? w1 : w0) + 1024 * (kWaves * k + wave));
+      dma16(wbase + (woff[k] + col), wbuf(b) + 1024 * (kWaves * k + wave));
     else
-      dma16(abase + (aoff[k - kWd] + col), (b ? a1 : a0) + 1024 * (kWaves * (k - kWd) + wave));
+      dma16(abase + (aoff[k - kWd] + col), abuf(b) + 1024 * (kWaves * (k - kWd) + wave));
   };
   auto dma_stage = [&](int q, auto bc) {
     const u32 col = stage_col(q);
@@ -191,8 +190,8 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM>::kThreads), 2) void w8a8_til
   };
   auto read_half = [&](Frags& f, auto bc, auto hc) {
     constexpr int b = decltype(bc)::value, hh = decltype(hc)::value;
-    const uint8_t* wt = (b ? w1 : w0) + wrow;
-    const uint8_t* at = (b ? a1 : a0) + arow;
+    const uint8_t* wt = wbuf(b) + wrow;
+    const uint8_t* at = abuf(b) + arow;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
 #pragma unroll
@@ -238,22 +237,28 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM>::kThreads), 2) void w8a8_til
 
   using B0 = std::integral_constant<int, 0>;
   using B1 = std::integral_constant<int, 1>;
+  using B2 = std::integral_constant<int, 2>;
+  using B3 = std::integral_constant<int, 3>;
   Frags f0, f1;
   dma_stage(0, B0{});
   dma_stage(1, B1{});
-  wait_vm_lds<kDmas>();
+  if constexpr (R > 2) dma_stage(2, B2{});
+  if constexpr (R > 3) dma_stage(3, B3{});
+  wait_vm_lds<(R - 1) * kDmas>();
   barrier();
   read_half(f0, B0{}, B0{});
   auto iteration = [&](int q, auto bc) {
     constexpr int b = decltype(bc)::value;
     using BC = std::integral_constant<int, b>;
-    using BN = std::integral_constant<int, 1 - b>;
+    using BN = std::integral_constant<int, (b + 1) % R>;
     __builtin_amdgcn_sched_barrier(0);
     read_half(f1, BC{}, B1{});
     mfma_half(f0);
     interleave(B0{});
-    const u32 col = stage_col(q + 2);
-    wait_vm_lds<0>();  // this wave's reads of the stage, and its DMAs of the next
+    const u32 col = stage_col(q + R);
+    // this wave's reads of the stage, and its DMAs of the next one; those of
+    // the R - 2 stages after it may still be in flight
+    wait_vm_lds<(R - 2) * kDmas>();
     barrier();
     __builtin_amdgcn_sched_barrier(0);
     read_half(f0, BN{}, B0{});
@@ -263,11 +268,17 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM>::kThreads), 2) void w8a8_til
     interleave(B1{});
   };
   int q = 0;
-  for (; q + 1 < S; q += 2) {
+  for (; q + R <= S; q += R) {
     iteration(q, B0{});
     iteration(q + 1, B1{});
+    if constexpr (R > 2) iteration(q + 2, B2{});
+    if constexpr (R > 3) iteration(q + 3, B3{});
   }
   if (q < S) iteration(q, B0{});
+  if constexpr (R > 2)
+    if (q + 1 < S) iteration(q + 1, B1{});
+  if constexpr (R > 3)
+    if (q + 2 < S) iteration(q + 2, B2{});
   if (half_end) mfma_half(f0);
   wait_vm_lds<0>();  // no LDS write may land after this
   barrier();         // every wave has finished its last LDS reads
@@ -377,48 +388,66 @@ struct Plan {
   int splits;
 };
 
+// Workgroup tiles, the test hook's name of each (channels / 64, tokens / 64, LDS
+// stages) and what a launch of it takes: with n workgroups on the busiest
+// compute unit, base + n (fill + S step) us for S stages of 128 k; where two
+// workgroups share a compute unit, base + (n / 2) (fill2 + S step2), an odd one
+// at fill and step.  Fitted to 80 shapes (65 to 4608 tokens, K 512 to 12288, N 256
+// to 12288) on MI355X, every tile and split timed: the plan's pick is within 0.7 %
+// (geometric mean) of the best measured one, 11 % at most.
+#define SVDQ_SHAPES(X)                                   \
+  X(442, 4, 2, 2, 4, 2, -6.15, 14.14, 1.10, 0.0, 0.0)    \
+  X(342, 3, 2, 2, 4, 2, -5.27, 12.31, 0.91, 0.0, 0.0)    \
+  X(432, 2, 3, 4, 2, 2, -4.20, 10.67, 0.91, 0.0, 0.0)    \
+  X(323, 3, 2, 2, 2, 3, -0.31, 7.67, 0.483, 0.0, 0.0)    \
+  X(224, 2, 2, 2, 2, 4, 1.04, 5.12, 0.363, 0.0, 0.0)     \
+  X(222, 2, 2, 2, 2, 2, 0.11, 4.51, 0.605, 6.06, 0.808)  \
+  X(124, 1, 2, 2, 2, 4, 2.15, 2.79, 0.259, 0.0, 0.0)     \
+  X(114, 1, 1, 2, 2, 4, 2.92, 1.82, 0.156, 2.11, 0.363)
 struct ShapeInfo {
-  int code;     // the test hook's name
-  int tn, tm, waves, wgs, sub;
-  double stage; // cost of a 128-wide k stage of one workgroup, in matrix-core cycles of a CU
+  int code, tn, tm, waves, wgs, sub;
+  double base, fill, step, fill2, step2;
 };
-template <int WI, int WJ, int WN, int WM>
-constexpr ShapeInfo info(int code, double stage) {
-  using S = Shape<WI, WJ, WN, WM>;
-  return ShapeInfo{code, S::kTN, S::kTM, S::kWaves, S::kWgs, S::kSub, stage};
+template <int WI, int WJ, int WN, int WM, int R>
+constexpr ShapeInfo info(int code, double base, double fill, double step, double fill2, double step2) {
+  using S = Shape<WI, WJ, WN, WM, R>;
+  return ShapeInfo{code, S::kTN, S::kTM, S::kWaves, S::kWgs, S::kSub, base, fill, step, fill2, step2};
 }
-constexpr ShapeInfo kShapes[] = {info<4, 2, 2, 4>(44, 2048), info<3, 2, 2, 4>(34, 1536), info<2, 3, 4, 2>(43, 1536),
-                                 info<2, 2, 4, 2>(42, 1100), info<2, 2, 2, 2>(22, 620)};
+#define SVDQ_INFO(code, wi, wj, wn, wm, r, base, fill, step, fill2, step2) \
+  info<wi, wj, wn, wm, r>(code, base, fill, step, fill2, step2),
+constexpr ShapeInfo kShapes[] = {SVDQ_SHAPES(SVDQ_INFO)};
+#undef SVDQ_INFO
+constexpr int kMaxSplits = 16;
 
 std::atomic<int> g_tile{0}, g_splits{0};  // test hook
 
-// The workgroup tile and the K-splits: the plan whose rounds of workgroups
-// cost least.
+// the cheapest tile and K-split
 Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int cus = current_cus();
-  const int S = (int)((K + 127) / 128);
+  const int stages = (int)((K + 127) / 128);
+  const int forced_tile = g_tile.load(std::memory_order_relaxed), forced = g_splits.load(std::memory_order_relaxed);
   Plan best{-1, 0, 1};
   double best_cost = 0;
-  const int forced_tile = g_tile.load(std::memory_order_relaxed), forced = g_splits.load(std::memory_order_relaxed);
   for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
     const ShapeInfo& s = kShapes[i];
     if (forced_tile > 1 && forced_tile != s.code) continue;
-    const int64_t tiles64 = ((N + s.tn - 1) / s.tn) * ((M + s.tm - 1) / s.tm);
-    if (tiles64 > (1 << 30)) continue;
-    const int tiles = (int)tiles64;
-    for (int splits = 1; splits <= 16 && splits <= S; splits *= 2) {
-      if (splits > 1 && (tiles * (int64_t)s.waves > (int64_t)kWsMaxCounters || (tiles >= 2 * cus && forced <= 1))) break;
-      if (forced > 0 && splits != forced && 2 * splits <= std::min(16, S) && splits < forced) continue;
-      if (forced > 0 && splits > forced) break;
-      const int64_t wgs = (int64_t)tiles * splits, slots = (int64_t)cus * s.wgs;
-      const int64_t rounds = (wgs + slots - 1) / slots;
-      const double stages = (double)((S + splits - 1) / splits);
-      const double area = s.tn * s.tm / 65536.0;
-      const double fill = 3000 + 16000 * area;
-      const double join = splits > 1 ? 3000 + (6000.0 + 3000.0 * splits) * area : 0.0;
-      const double cost = rounds * s.wgs * (stages * s.stage + fill + join);
-      if (best.shape < 0 || cost < best_cost) {
-        best = Plan{i, tiles, splits};
+    const int64_t tiles = ((N + s.tn - 1) / s.tn) * ((M + s.tm - 1) / s.tm);
+    if (tiles > (1 << 30)) continue;
+    for (int splits = 1; splits <= std::min(kMaxSplits, stages); splits *= 2) {
+      const int64_t wgs = tiles * splits;
+      if (splits > 1 && tiles * s.waves > (int64_t)kWsMaxCounters) break;
+      if (forced > 0 ? splits > forced : splits > 1 && wgs > 2 * cus) break;
+      const double n = (double)((wgs + cus - 1) / cus), S = (double)((stages + splits - 1) / splits);
+      double cost = s.base;
+      if (s.wgs == 2) {
+        const double pairs = std::floor(n / 2);
+        cost += pairs * (s.fill2 + S * s.step2) + (n - 2 * pairs) * (s.fill + S * s.step);
+      } else {
+        cost += n * (s.fill + S * s.step);
+      }
+      if (splits > 1) cost += 2.65 + 0.53 * splits + 0.58 * (s.tn / 64) * (s.tm / 64);  // the partials' round trips
+      if (best.shape < 0 || cost < best_cost || (forced > 0 && best.shape == i)) {
+        best = Plan{i, (int)tiles, splits};
         best_cost = cost;
       }
     }
@@ -426,30 +455,40 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
-template <int WI, int WJ, int WN, int WM>
+template <int WI, int WJ, int WN, int WM, int R>
 void tile_go(const TileArgs& t, int tiles, hipStream_t stream) {
-  const dim3 block(Shape<WI, WJ, WN, WM>::kThreads);
+  const dim3 block(Shape<WI, WJ, WN, WM, R>::kThreads);
   if (t.splits > 1)
-    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, WN, WM, true>), dim3(tiles, t.splits), block, 0, stream, t);
+    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, WN, WM, R, true>), dim3(tiles, t.splits), block, 0, stream, t);
   else
-    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, WN, WM, false>), dim3(tiles), block, 0, stream, t);
+    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, WN, WM, R, false>), dim3(tiles), block, 0, stream, t);
 }
 
 }  // namespace
+
+bool w8a8_tile_known(int tile) {
+  if (tile == 0 || tile == 1) return true;
+  for (const ShapeInfo& s : kShapes)
+    if (s.code == tile) return true;
+  return false;
+}
 
 void set_w8a8_plan_override(int tile, int splits) {
   g_tile.store(tile, std::memory_order_relaxed);
   g_splits.store(splits, std::memory_order_relaxed);
 }
 
-// up to 64 tokens run on the weight-streaming kernel
-static bool few_tokens(int64_t M) {
+// The weight-streaming kernel for up to 4 tokens, and up to 16 where its workgroups
+// (one per 16 channels) are fewer than two per compute unit.  Measured, it against the
+// best tile: 1 token 3072 -> 3072 5.5 / 7.3 us, 3072 -> 12288 9.6 / 9.8, 12288 -> 3072 10.5 / 14.7;
+// 16 tokens 6.3 / 7.4, 12.1 / 10.2, 14.4 / 15.1.
+static bool few_tokens(int64_t M, int64_t N) {
   const int t = g_tile.load(std::memory_order_relaxed);
-  return M <= 64 && t <= 1;
+  return t == 1 ? M <= 16 : t == 0 && (M <= 4 || (M <= 16 && N / 16 < 2 * current_cus()));
 }
 
 size_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (few_tokens(M)) return 0;
+  if (few_tokens(M, N)) return 0;
   const Plan p = plan_of(M, N, K);
   if (p.splits == 1) return 0;
   const ShapeInfo& s = kShapes[p.shape];
@@ -457,7 +496,7 @@ size_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 }
 
 hipError_t launch_w8a8_gemm(const W8a8Args& a, Workspace ws, hipStream_t stream) {
-  if (few_tokens(a.M)) return launch_w8a8_skinny(a, stream);
+  if (few_tokens(a.M, a.N)) return launch_w8a8_skinny(a, stream);
   const Plan p = plan_of(a.M, a.N, a.K);
   if (p.splits > 1 && ws.bytes < w8a8_workspace_bytes(a.M, a.N, a.K)) return hipErrorInvalidValue;
   TileArgs t{a, p.splits, nullptr, nullptr};
@@ -466,11 +505,10 @@ hipError_t launch_w8a8_gemm(const W8a8Args& a, Workspace ws, hipStream_t stream)
     t.part = static_cast<int*>(ws_scratch(ws));
   }
   switch (kShapes[p.shape].code) {
-    case 44: tile_go<4, 2, 2, 4>(t, p.tiles, stream); break;
-    case 34: tile_go<3, 2, 2, 4>(t, p.tiles, stream); break;
-    case 43: tile_go<2, 3, 4, 2>(t, p.tiles, stream); break;
-    case 42: tile_go<2, 2, 4, 2>(t, p.tiles, stream); break;
-    case 22: tile_go<2, 2, 2, 2>(t, p.tiles, stream); break;
+#define SVDQ_GO(code, wi, wj, wn, wm, r, base, fill, step, fill2, step2) \
+  case code: tile_go<wi, wj, wn, wm, r>(t, p.tiles, stream); break;
+    SVDQ_SHAPES(SVDQ_GO)
+#undef SVDQ_GO
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();

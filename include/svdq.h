@@ -488,11 +488,12 @@ size_t svdq_w8a8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
 
 /*
  * Test hook for svdq_w8a8_gemm: the kernel and its split for every later call in
- * this process.  tile 0 chooses by shape, 1 the few-token kernel where M <= 64,
- * 22, 42, 43, 34 and 44 the tile kernel with workgroup tiles of 128 x 128, 256 x 128,
- * 256 x 192, 192 x 256 and 256 x 256 (channels x tokens); splits 0 by shape, else the K-splits per tile
- * (rounded to a power of two that the K stages allow).  Y does not change.  Query
- * the workspace size after setting it.  INVALID_VALUE for other values.
+ * this process.  tile 0 chooses by shape, 1 the few-token kernel where M <= 16; 114,
+ * 124, 222, 224, 323, 432, 342 and 442 the tile kernel, the digits being the workgroup
+ * tile's channels / 64, its tokens / 64 and its LDS stages; splits 0 by shape, else
+ * the K-splits per tile (1..16; the largest power of two up to it that the K stages
+ * allow).  Y does not change.  Query the workspace size after setting it.
+ * INVALID_VALUE for other values.
  */
 svdq_status svdq_debug_set_w8a8_plan(int tile, int splits);
 

@@ -204,3 +204,26 @@ def test_packed_linear():
         0.25 * K * ws.astype(float)[:, None] * pk["w_scales"].astype(float)[None]
     xh = np.abs(x / sm) @ np.abs(w * sm).T
     assert (np.abs(y - ref) <= 1.02 * step + 2 * HALF_BF16 * xh).all()
+
+
+@pytest.mark.parametrize("tile", [1, 114, 124, 222, 224, 323, 342, 432, 442])
+@pytest.mark.parametrize("splits", [1, 2, 16])
+def test_every_tile_and_split(tile, splits):
+    """The same shapes on every kernel, tile and split give the same bits: one
+    stage and less, an odd number of stages, a half one at the end, ragged
+    tokens and channels."""
+    import torch
+    import bit_diffusion_transformer_svdq_amd as P
+    for M, N, K in [(9, 64, 64), (16, 192, 192), (70, 320, 448), (300, 576, 1088), (129, 448, 2176), (129, 448, 4096)]:
+        if tile == 1 and M > 16:
+            continue
+        c = _gemm_case(M, N, K, 9)
+        d = (dev(c[0]), dev(c[1]), dev(c[2]), dev(c[3]), dev_bf16(c[4]))
+        want = P.w8a8_gemm(*d, epilogue="gelu_tanh")
+        P.debug_set_w8a8_plan(tile, splits)
+        try:
+            got = P.w8a8_gemm(*d, epilogue="gelu_tanh")
+        finally:
+            P.debug_set_w8a8_plan()
+        assert torch.equal(got, want), (M, N, K)
+        _check_gemm(host(got), *c[:4], c[4], "gelu_tanh")

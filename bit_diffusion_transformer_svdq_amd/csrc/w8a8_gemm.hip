@@ -5,14 +5,14 @@
 // von Diffusionsmodellen durch Nunchaku 4-Bit-Quantisierung", section "Nunchaku
 // Lite: Nahtlose Integration in Diffusers": precision-sensitive layers).
 //
-// With no dequantization inside the K loop the kernel is a plain int8 GEMM, and
-// what bounds it is the matrix core (2 M N K / 5 POP/s) next to the LDS: a k
-// stage of 128 bytes per row costs the LDS its DMA writes plus each operand row
-// once per wave that needs it, so the wave tile is as large as the registers
-// allow.
-//  * workgroup tile 64 WI weight rows x 64 WJ token rows, 4 waves as 2 x 2, each
-//    32 WI x 32 WJ = WI x WJ tiles of v_mfma_i32_32x32x32_i8 (WI = WJ = 4: 256
-//    int32 accumulators per lane, one wave per SIMD);
+// With no dequantization inside the K loop the kernel is a plain int8 GEMM.  Large
+// products are bound by the chip's power: on random codes registers alone feed
+// v_mfma_i32_32x32x32_i8 at 3.45 POP/s and v_mfma_i32_16x16x64_i8, which touches its
+// accumulators half as often, at 4.15 (4.9 on zeros), so the second is used, and
+// operands are moved as little as the registers allow.
+//  * workgroup tile 32 WI WN weight rows x 32 WJ WM token rows, WN x WM waves of
+//    2 WI x 2 WJ tiles of 16 x 16 (256 x 256 on 8 waves: 128 int32 accumulators per
+//    lane, two waves per SIMD);
 //  * R LDS stages of 128 bytes per row, filled by global_load_lds_dwordx4 with
 //    8 whole 128-byte row runs per instruction.  A stage is computed in two
 //    halves: while the MFMAs of the first run, the fragments of the second are
@@ -28,8 +28,8 @@
 //    caller's workspace (integer sums: the order does not matter).
 //
 // The MFMA A operand is the weight tile (rows n), B the token tile (columns m),
-// so lane l holds Y[m = l % 32][n = 8 k + 4 (l / 32) + v] of each 32 x 32 tile; Y
-// leaves through LDS in runs of 64 WI bytes per row.
+// so lane l holds Y[m = l % 16][n = 4 (l / 16) + v] of each 16 x 16 tile; Y leaves
+// through LDS in runs of 64 WI bytes per row.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -46,9 +46,9 @@ namespace svdq {
 namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v16i __attribute__((ext_vector_type(16)));
 typedef unsigned v4u __attribute__((ext_vector_type(4)));
 typedef unsigned int u32;
+typedef u32 u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) void glb_void;
 
@@ -140,8 +140,8 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wn = wave / WM;
   const int wm = wave % WM;
-  const int l32 = lane & 31;
-  const int lp = lane >> 5;
+  const int l16 = lane & 15;
+  const int lq = lane >> 4;
 
   // DMA role: instruction k of a wave fills rows 8 (waves k + wave) + lane / 8, slot
   // lane % 8 of each row, with granule (lane % 8) ^ row[3:1].  Rows past the
@@ -153,76 +153,74 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
   const u32 back = (K & 64) != 0 && gran >= 64 ? 64u : 0u;
   constexpr int kWd = kTN / (8 * kWaves), kAd = kTM / (8 * kWaves);  // DMAs per stage and wave
   static_assert(kWaves % 2 == 0 && kWd * 8 * kWaves == kTN && kAd * 8 * kWaves == kTM, "whole row runs per wave");
+  // (N % 64 == 0: the 8 weight rows of an instruction are all inside or all
+  // past the end, so their offset is uniform)
   u32 woff[kWd], aoff[kAd];
+  const u32 wlane = (u32)(lane >> 3) * (u32)K + gran;
 #pragma unroll
   for (int k = 0; k < kWd; ++k)
-    woff[k] = (u32)(min(n0 + 8 * (kWaves * k + wave) + (lane >> 3), N - 1) - n0) * (u32)K + gran;
+    woff[k] = (u32)__builtin_amdgcn_readfirstlane(min(n0 + 8 * (kWaves * k + wave), N - 8) - n0) * (u32)K;
 #pragma unroll
   for (int k = 0; k < kAd; ++k)
     aoff[k] = (u32)(min(m0 + 8 * (kWaves * k + wave) + (lane >> 3), M - 1) - m0) * (u32)K + gran;
-  // column of stage q (counted from q_begin; past the end the last stage again)
+  // column of stage q (counted from q_begin; past the end the last stage again), and
+  // how far back the lane's granule lies in it
   auto stage_col = [&](int q) {
     const int s = min(q_begin + q, q_end - 1);
-    return 128u * (u32)s - (s == S_all - 1 ? back : 0u);
+    return u32x2{128u * (u32)s, s == S_all - 1 ? back : 0u};
   };
   constexpr int kDmas = kWd + kAd;
-  auto dma_one = [&](int k, u32 col, auto bc) {
+  auto dma_one = [&](int k, u32x2 col, auto bc) {
     constexpr int b = decltype(bc)::value;
     if (k < kWd)
-      dma16(wbase + (woff[k] + col), wbuf(b) + 1024 * (kWaves * k + wave));
+      dma16(wbase + (woff[k] + col.x) + (wlane - col.y), wbuf(b) + 1024 * (kWaves * k + wave));
     else
-      dma16(abase + (aoff[k - kWd] + col), abuf(b) + 1024 * (kWaves * (k - kWd) + wave));
+      dma16(abase + col.x + (aoff[k - kWd] - col.y), abuf(b) + 1024 * (kWaves * (k - kWd) + wave));
   };
   auto dma_stage = [&](int q, auto bc) {
-    const u32 col = stage_col(q);
+    const u32x2 col = stage_col(q);
 #pragma unroll
     for (int k = 0; k < kDmas; ++k) dma_one(k, col, bc);
   };
 
-  // Fragment reads: lane (l32, lp) takes granule 2 ks + lp of rows 32 i + l32 for
-  // k step ks (32 k); half hh holds steps 2 hh and 2 hh + 1.
-  int fo[4];
+  // Fragment reads: lane (l16, lq) takes granule 4 hh + lq of rows 16 i + l16 for
+  // half hh, a k step of 64.
+  constexpr int kI = 2 * WI, kJ = 2 * WJ;  // 16 x 16 tiles of a wave
+  int fo[2];
 #pragma unroll
-  for (int ks = 0; ks < 4; ++ks) fo[ks] = 128 * l32 + 16 * ((2 * ks + lp) ^ ((l32 >> 1) & 7));
+  for (int hh = 0; hh < 2; ++hh) fo[hh] = 128 * l16 + 16 * ((4 * hh + lq) ^ (l16 >> 1));
   const int wrow = wn * 32 * WI * 128, arow = wm * 32 * WJ * 128;
   struct Frags {
-    v4i w[2][WI], a[2][WJ];
+    v4i w[kI], a[kJ];
   };
   auto read_half = [&](Frags& f, auto bc, auto hc) {
     constexpr int b = decltype(bc)::value, hh = decltype(hc)::value;
     const uint8_t* wt = wbuf(b) + wrow;
     const uint8_t* at = abuf(b) + arow;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
+    for (int i = 0; i < kI; ++i) f.w[i] = *reinterpret_cast<const v4i*>(wt + fo[hh] + 2048 * i);
 #pragma unroll
-      for (int i = 0; i < WI; ++i) f.w[s][i] = *reinterpret_cast<const v4i*>(wt + fo[2 * hh + s] + 4096 * i);
-#pragma unroll
-      for (int j = 0; j < WJ; ++j) f.a[s][j] = *reinterpret_cast<const v4i*>(at + fo[2 * hh + s] + 4096 * j);
-    }
+    for (int j = 0; j < kJ; ++j) f.a[j] = *reinterpret_cast<const v4i*>(at + fo[hh] + 2048 * j);
   };
 
-  v16i acc[WI][WJ];
+  v4i acc[kI][kJ];
 #pragma unroll
-  for (int i = 0; i < WI; ++i)
+  for (int i = 0; i < kI; ++i)
 #pragma unroll
-    for (int j = 0; j < WJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+    for (int j = 0; j < kJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
   auto mfma_half = [&](const Frags& f) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int i = 0; i < kI; ++i)
 #pragma unroll
-      for (int i = 0; i < WI; ++i)
-#pragma unroll
-        for (int j = 0; j < WJ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[s][i], f.a[s][j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < kJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[i], f.a[j], acc[i][j], 0, 0, 0);
   };
   // One LDS read (two where there are more of them than MFMAs) after each of
   // the first MFMAs of a half; in the second half the DMAs are spread over the
   // MFMAs, so that the waves do not queue for the address unit while the matrix
   // core idles.
   auto interleave = [&](auto with_dma) {
-    constexpr int kReads = 2 * (WI + WJ), kMfmas = 2 * WI * WJ;
+    constexpr int kReads = kI + kJ, kMfmas = kI * kJ;
     constexpr int kRead = (kReads + kMfmas - 1) / kMfmas;
     constexpr int kEvery = kMfmas / kDmas > 0 ? kMfmas / kDmas : 1, kDma = (kDmas * kEvery + kMfmas - 1) / kMfmas;
 #pragma unroll
@@ -255,7 +253,7 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
     read_half(f1, BC{}, B1{});
     mfma_half(f0);
     interleave(B0{});
-    const u32 col = stage_col(q + R);
+    const u32x2 col = stage_col(q + R);
     // this wave's reads of the stage, and its DMAs of the next one; those of
     // the R - 2 stages after it may still be in flight
     wait_vm_lds<(R - 2) * kDmas>();
@@ -291,12 +289,12 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
     const size_t sub = ((size_t)tm * ((N + kTN - 1) / kTN) + tn) * kWaves + wave;
     int* mine = p.part + (sub * p.splits + blockIdx.y) * kSub + lane;
 #pragma unroll
-    for (int i = 0; i < WI; ++i)
+    for (int i = 0; i < kI; ++i)
 #pragma unroll
-      for (int j = 0; j < WJ; ++j)
+      for (int j = 0; j < kJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          __hip_atomic_store(mine + (((i * WJ + j) * 16 + e) << 6), acc[i][j][e], __ATOMIC_RELAXED,
+        for (int e = 0; e < 4; ++e)
+          __hip_atomic_store(mine + (((i * kJ + j) * 4 + e) << 6), acc[i][j][e], __ATOMIC_RELAXED,
                              __HIP_MEMORY_SCOPE_AGENT);
     __asm__ volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): the partial is visible to the agent
@@ -310,15 +308,16 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
       if (s == (int)blockIdx.y) continue;
       const int* src = p.part + (sub * p.splits + s) * kSub + lane;
 #pragma unroll
-      for (int i = 0; i < WI; ++i)
+      for (int i = 0; i < kI; ++i) {
+        v4i t[kJ];
 #pragma unroll
-        for (int j = 0; j < WJ; ++j) {
-          v16i t;
+        for (int j = 0; j < kJ; ++j)
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            t[e] = __hip_atomic_load(src + (((i * WJ + j) * 16 + e) << 6), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          acc[i][j] += t;
-        }
+          for (int e = 0; e < 4; ++e)
+            t[j][e] = __hip_atomic_load(src + (((i * kJ + j) * 4 + e) << 6), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) acc[i][j] += t[j];
+      }
     }
   }
 
@@ -333,38 +332,35 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
   const int sb = wave / kPerBuf;
   uint8_t* stage = (sb == 0 ? w0 : sb == 1 ? w1 : sb == 2 ? a0 : a1) + (wave % kPerBuf) * 2 * Sh::kSub;
   const int nw = n0 + wn * 32 * WI, mw = m0 + wm * 32 * WJ;  // the wave's first column and row
-  float sx[WJ];
+  float sx[kJ];
 #pragma unroll
-  for (int j = 0; j < WJ; ++j) sx[j] = p.g.act_scales[min(mw + 32 * j + l32, M - 1)];
+  for (int j = 0; j < kJ; ++j) sx[j] = p.g.act_scales[min(mw + 16 * j + l16, M - 1)];
 #pragma unroll
-  for (int i = 0; i < WI; ++i)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int nl = 32 * i + 8 * k + 4 * lp;  // within the wave's columns
-      const int nc = min(nw + nl, N - 4);
-      const float4 sw = *reinterpret_cast<const float4*>(p.g.w_scales + nc);
-      float bb[4] = {0.f, 0.f, 0.f, 0.f};
-      if (p.g.bias != nullptr) {
-        const uint2 b2 = *reinterpret_cast<const uint2*>(p.g.bias + nc);
-        bb[0] = bf16_lo(b2.x), bb[1] = bf16_hi(b2.x), bb[2] = bf16_lo(b2.y), bb[3] = bf16_hi(b2.y);
-      }
-#pragma unroll
-      for (int j = 0; j < WJ; ++j) {
-        float o[4] = {(float)acc[i][j][4 * k], (float)acc[i][j][4 * k + 1], (float)acc[i][j][4 * k + 2],
-                      (float)acc[i][j][4 * k + 3]};
-        o[0] = __builtin_fmaf(o[0], sx[j] * sw.x, bb[0]);
-        o[1] = __builtin_fmaf(o[1], sx[j] * sw.y, bb[1]);
-        o[2] = __builtin_fmaf(o[2], sx[j] * sw.z, bb[2]);
-        o[3] = __builtin_fmaf(o[3], sx[j] * sw.w, bb[3]);
-        if (p.g.epilogue == kEpilogueGelu) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) o[v] = gelu_exp2(o[v]);
-        }
-        const int ml = 32 * j + l32;
-        uint8_t* dst = stage + ml * (16 * kChunks) + (((nl >> 3) ^ (ml & kMask)) << 4) + 8 * lp;
-        *reinterpret_cast<uint2*>(dst) = uint2{pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3])};
-      }
+  for (int i = 0; i < kI; ++i) {
+    const int nl = 16 * i + 4 * lq;  // within the wave's columns
+    const int nc = min(nw + nl, N - 4);
+    const float4 sw = *reinterpret_cast<const float4*>(p.g.w_scales + nc);
+    float bb[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.g.bias != nullptr) {
+      const uint2 b2 = *reinterpret_cast<const uint2*>(p.g.bias + nc);
+      bb[0] = bf16_lo(b2.x), bb[1] = bf16_hi(b2.x), bb[2] = bf16_lo(b2.y), bb[3] = bf16_hi(b2.y);
     }
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      float o[4];
+      o[0] = __builtin_fmaf((float)acc[i][j][0], sx[j] * sw.x, bb[0]);
+      o[1] = __builtin_fmaf((float)acc[i][j][1], sx[j] * sw.y, bb[1]);
+      o[2] = __builtin_fmaf((float)acc[i][j][2], sx[j] * sw.z, bb[2]);
+      o[3] = __builtin_fmaf((float)acc[i][j][3], sx[j] * sw.w, bb[3]);
+      if (p.g.epilogue == kEpilogueGelu) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[v] = gelu_exp2(o[v]);
+      }
+      const int ml = 16 * j + l16;
+      uint8_t* dst = stage + ml * (16 * kChunks) + (((nl >> 3) ^ (ml & kMask)) << 4) + 8 * (lq & 1);
+      *reinterpret_cast<uint2*>(dst) = uint2{pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3])};
+    }
+  }
   __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes are done
   __asm__ volatile("" ::: "memory");
   // chunk by chunk in row order: an instruction stores 64 chunks, whole rows of
@@ -386,6 +382,7 @@ struct Plan {
   int shape;    // index into kShapes
   int tiles;
   int splits;
+  double cost;  // us, by the model below
 };
 
 // Workgroup tiles, the test hook's name of each (channels / 64, tokens / 64, LDS
@@ -396,14 +393,14 @@ struct Plan {
 // to 12288) on MI355X, every tile and split timed: the plan's pick is within 0.7 %
 // (geometric mean) of the best measured one, 11 % at most.
 #define SVDQ_SHAPES(X)                                   \
-  X(442, 4, 2, 2, 4, 2, -6.15, 14.14, 1.10, 0.0, 0.0)    \
-  X(342, 3, 2, 2, 4, 2, -5.27, 12.31, 0.91, 0.0, 0.0)    \
-  X(432, 2, 3, 4, 2, 2, -4.20, 10.67, 0.91, 0.0, 0.0)    \
-  X(323, 3, 2, 2, 2, 3, -0.31, 7.67, 0.483, 0.0, 0.0)    \
-  X(224, 2, 2, 2, 2, 4, 1.04, 5.12, 0.363, 0.0, 0.0)     \
-  X(222, 2, 2, 2, 2, 2, 0.11, 4.51, 0.605, 6.06, 0.808)  \
-  X(124, 1, 2, 2, 2, 4, 2.15, 2.79, 0.259, 0.0, 0.0)     \
-  X(114, 1, 1, 2, 2, 4, 2.92, 1.82, 0.156, 2.11, 0.363)
+  X(442, 4, 2, 2, 4, 2, -4.89, 13.11, 1.107, 0.0, 0.0)   \
+  X(342, 3, 2, 2, 4, 2, -4.51, 11.32, 0.940, 0.0, 0.0)   \
+  X(432, 2, 3, 4, 2, 2, -3.25, 9.60, 0.936, 0.0, 0.0)    \
+  X(323, 3, 2, 2, 2, 3, 0.26, 6.76, 0.565, 0.0, 0.0)     \
+  X(224, 2, 2, 2, 2, 4, 1.08, 5.02, 0.380, 0.0, 0.0)     \
+  X(222, 2, 2, 2, 2, 2, 0.39, 4.13, 0.618, 5.95, 0.756)  \
+  X(124, 1, 2, 2, 2, 4, 2.03, 2.69, 0.259, 0.0, 0.0)     \
+  X(114, 1, 1, 2, 2, 4, 3.12, 1.31, 0.163, 2.02, 0.360)
 struct ShapeInfo {
   int code, tn, tm, waves, wgs, sub;
   double base, fill, step, fill2, step2;
@@ -426,8 +423,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
   const int cus = current_cus();
   const int stages = (int)((K + 127) / 128);
   const int forced_tile = g_tile.load(std::memory_order_relaxed), forced = g_splits.load(std::memory_order_relaxed);
-  Plan best{-1, 0, 1};
-  double best_cost = 0;
+  Plan best{-1, 0, 1, 0.0};
   for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
     const ShapeInfo& s = kShapes[i];
     if (forced_tile > 1 && forced_tile != s.code) continue;
@@ -446,10 +442,37 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
         cost += n * (s.fill + S * s.step);
       }
       if (splits > 1) cost += 2.65 + 0.53 * splits + 0.58 * (s.tn / 64) * (s.tm / 64);  // the partials' round trips
-      if (best.shape < 0 || cost < best_cost || (forced > 0 && best.shape == i)) {
-        best = Plan{i, (int)tiles, splits};
-        best_cost = cost;
-      }
+      if (best.shape < 0 || cost < best.cost || (forced > 0 && best.shape == i)) best = Plan{i, (int)tiles, splits, cost};
+    }
+  }
+  return best;
+}
+
+// The launches of a product: the tokens [0, m1) in whole rounds of one of the
+// largest tiles, and the rest on the tile that suits it (m1 = M: one launch).  The
+// last round of a large tile otherwise leaves most compute units idle (4608 tokens,
+// 3072 -> 12288: 864 tiles of 256 x 256 are 3.4 rounds; 768 and then 256 of 192 x 128 are 4
+// full ones, the last of them a short one).
+struct Launches {
+  int64_t m1;
+  Plan first, rest;
+};
+Launches launches_of(int64_t M, int64_t N, int64_t K) {
+  Launches best{M, plan_of(M, N, K), Plan{}};
+  if (g_tile.load(std::memory_order_relaxed) > 1 || g_splits.load(std::memory_order_relaxed) > 0) return best;
+  const int cus = current_cus();
+  const double S = (double)((K + 127) / 128);
+  double best_cost = best.first.cost;
+  for (int i = 0; i < 3; ++i) {
+    const ShapeInfo& s = kShapes[i];
+    const int64_t nt = (N + s.tn - 1) / s.tn, mt = (M + s.tm - 1) / s.tm;
+    const int64_t rounds = nt * mt / cus, mt1 = rounds * cus / nt;
+    if (nt * mt > (1 << 30) || mt1 <= 0 || mt1 * s.tm >= M) continue;
+    Launches l{mt1 * s.tm, Plan{i, (int)(mt1 * nt), 1, 0.0}, plan_of(M - mt1 * s.tm, N, K)};
+    l.first.cost = s.base + (double)((mt1 * nt + cus - 1) / cus) * (s.fill + S * s.step);
+    if (l.first.cost + l.rest.cost < best_cost) {
+      best = l;
+      best_cost = l.first.cost + l.rest.cost;
     }
   }
   return best;
@@ -487,18 +510,20 @@ static bool few_tokens(int64_t M, int64_t N) {
   return t == 1 ? M <= 16 : t == 0 && (M <= 4 || (M <= 16 && N / 16 < 2 * current_cus()));
 }
 
-size_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  if (few_tokens(M, N)) return 0;
-  const Plan p = plan_of(M, N, K);
-  if (p.splits == 1) return 0;
+static size_t plan_bytes(const Plan& p) {
+  if (p.splits <= 1) return 0;
   const ShapeInfo& s = kShapes[p.shape];
   return ws_bytes((size_t)p.tiles * s.waves, (size_t)p.tiles * s.waves * p.splits * s.sub * sizeof(int));
 }
 
-hipError_t launch_w8a8_gemm(const W8a8Args& a, Workspace ws, hipStream_t stream) {
-  if (few_tokens(a.M, a.N)) return launch_w8a8_skinny(a, stream);
-  const Plan p = plan_of(a.M, a.N, a.K);
-  if (p.splits > 1 && ws.bytes < w8a8_workspace_bytes(a.M, a.N, a.K)) return hipErrorInvalidValue;
+size_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (few_tokens(M, N)) return 0;
+  const Launches l = launches_of(M, N, K);
+  return std::max(plan_bytes(l.first), l.m1 < M ? plan_bytes(l.rest) : 0);
+}
+
+static hipError_t launch_plan(const W8a8Args& a, const Plan& p, const Workspace& ws, hipStream_t stream) {
+  if (plan_bytes(p) > ws.bytes) return hipErrorInvalidValue;
   TileArgs t{a, p.splits, nullptr, nullptr};
   if (p.splits > 1) {
     t.count = ws_counters(ws);
@@ -512,6 +537,20 @@ hipError_t launch_w8a8_gemm(const W8a8Args& a, Workspace ws, hipStream_t stream)
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
+}
+
+hipError_t launch_w8a8_gemm(const W8a8Args& a, Workspace ws, hipStream_t stream) {
+  if (few_tokens(a.M, a.N)) return launch_w8a8_skinny(a, stream);
+  const Launches l = launches_of(a.M, a.N, a.K);
+  W8a8Args part = a;
+  part.M = (int)l.m1;
+  const hipError_t e = launch_plan(part, l.first, ws, stream);
+  if (e != hipSuccess || l.m1 == a.M) return e;
+  part.M = (int)(a.M - l.m1);
+  part.act += (size_t)l.m1 * (size_t)a.K;
+  part.act_scales += l.m1;
+  part.y += (size_t)l.m1 * (size_t)a.N;
+  return launch_plan(part, l.rest, ws, stream);
 }
 
 }  // namespace svdq

@@ -33,15 +33,15 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 inline svdq_status check_current_device() {
   int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) return svdq_check_device(dev);  // cached per device
+  (void)hipGetLastError();
   int count = 0;
-  hipError_t e = hipGetDeviceCount(&count);
-  if (e != hipSuccess || count <= 0) {
+  if (hipGetDeviceCount(&count) != hipSuccess || count <= 0) {
     (void)hipGetLastError();
     return fail(SVDQ_STATUS_NO_DEVICE, "no HIP device visible");
   }
-  e = hipGetDevice(&dev);
-  if (e != hipSuccess) return fail(SVDQ_STATUS_HIP_ERROR, "hipGetDevice: %s", hipGetErrorString(e));
-  return svdq_check_device(dev);
+  return fail(SVDQ_STATUS_HIP_ERROR, "hipGetDevice: %s", hipGetErrorString(e));
 }
 
 // A device byte range an entry point reads or writes.  Inputs may share memory

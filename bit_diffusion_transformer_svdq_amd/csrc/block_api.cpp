@@ -196,10 +196,10 @@ svdq_status svdq_gate_norm_modulate(const void* x, int stream_type, int64_t x_st
   if (x_stride % 8 != 0 || (has_y && (y_stride % 8 != 0 || h_stride % 8 != 0)) ||
       (gate && gate_rows > 1 && gate_stride % 8 != 0) || (mod && mod_rows > 1 && mod_stride % 8 != 0))
     return fail(SVDQ_STATUS_NOT_SUPPORTED, "row strides must be multiples of 8 elements");
-  const int64_t far = 1ll << 40;
+  const int64_t far = 1ll << 37;  // 2^24 rows of 4 bytes stay below 2^63
   if (x_stride > far || (has_y && (y_stride > far || h_stride > far)) || (gate && gate_rows > 1 && gate_stride > far) ||
       (mod && mod_rows > 1 && mod_stride > far))
-    return fail(SVDQ_STATUS_NOT_SUPPORTED, "a row stride is above 2^40");
+    return fail(SVDQ_STATUS_NOT_SUPPORTED, "a row stride is above 2^37");
   for (const void* p : {x, y, post_weight, gate, weight, scale, shift, (const void*)smooth, (const void*)h,
                         (const void*)z, (const void*)z_scales})
     if (bad_ptr(p)) return fail(SVDQ_STATUS_INVALID_VALUE, "device pointers must be 16-byte aligned");

@@ -526,7 +526,7 @@ svdq_status svdq_debug_set_w8a8_plan(int tile, int splits);
  *   smooth       device, fp32 [C] or NULL (int8 output only)
  * Strides are in elements and multiples of 8 (the chunks of a modulation
  * projection's output are rows of a larger stride); strides of arrays with one
- * row are not read.  C % 8 == 0, C % 64 == 0 for int8, C <= 32768, M <= 2^24
+ * row are not read.  C % 8 == 0, C % 64 == 0 for int8, C <= 32768, M <= 2^24, strides <= 2^37
  * (NOT_SUPPORTED beyond); M == 0 is a no-op; INVALID_VALUE for an unknown enum
  * value, a vector without the part it belongs to, a bad eps or
  * residual_scale, rows that do not divide M, and as for the other calls.
@@ -571,7 +571,7 @@ svdq_status svdq_gate_norm_modulate(
  *   q_out, k_out    device out, as q and k, strides of their own; may be q and k
  *              themselves with the same strides (in place)
  * head_dim % 8 == 0 and <= 256; for SVDQ_ROPE_HALVES R % 8 == 0; at most 4096 heads
- * each, M <= 2^24 (NOT_SUPPORTED beyond); theta finite and > 1; M == 0 is a no-op.
+ * each, M <= 2^24, strides <= 2^38 (NOT_SUPPORTED beyond); theta finite and > 1; M == 0 is a no-op.
  */
 typedef enum { SVDQ_POSITIONS_FP32 = 0, SVDQ_POSITIONS_INT32 = 1 } svdq_position_type;
 typedef enum { SVDQ_SPECTRUM_AXIS = 0, SVDQ_SPECTRUM_SHARED = 1 } svdq_spectrum;

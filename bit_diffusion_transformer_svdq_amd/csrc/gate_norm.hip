@@ -20,7 +20,7 @@
 // the shared vectors in registers and the next row in flight lost more to
 // occupancy than they saved (4608 x 3072: 23.6-26 us against 22.7).  Only with a
 // smoothing vector, whose reciprocals are the dearest part, a workgroup takes a
-// run of rows and keeps the reciprocals (quantizer 4608 x 3072: 16.2 -> 11.2 us).
+// run of rows and keeps the reciprocals (quantizer 4608 x 3072: 16.2 -> 11.3 us).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(threads_of<W>()) void gate_norm_kernel(const GateNo
 // q = rint(x_hat fl32(1/s)).  The row is kept as packed bf16.
 template <int W, int V, bool kSmooth>
 __global__ __launch_bounds__(threads_of<W>()) void quant_int8_kernel(const QuantInt8Args a) {
-  constexpr bool kKeep = V <= 2;  // reciprocals stay in registers over the run of rows
+  constexpr bool kKeep = V <= 3;  // reciprocals stay in registers over the run of rows
   __shared__ float red_all[W > 1 ? 2 * W : 1];
   const int row0 = first_row<W>(a.run), row_end = min(row0 + a.run, a.M);
   if (row0 >= row_end) return;
@@ -385,10 +385,12 @@ int waves_for(int64_t M, int c8, int per_lane) {
 //  gate norm  4608 x 1536: W1V3 15.0, W2V2 14.7, W4V1 13.8*    4608 x 5120: W4V3 41.1*, W8V2 46.4
 //             4608 x 3072: W2V3 24.7, W4V2 24.5, W8V1 24.2*    4608 x 4096: W2V4 36.5, W4V2 31.4, W8V1 31.2*
 //             8346 x 2304 fp32: W2V3 49.8*, W4V2 50.8          2304 x 8192: W4V4 35.1, W8V2 33.3*
-//  quantizer  4608 x 3072: W1V6 8.6*, W4V2 9.1, W8V1 10.1;  smoothed: W1V6 16.0, W2V3 13.8, W4V2 11.2*
-//             4608 x 12288: W4V6 29.2, W8V3 28.2*, W16V2 30.8;  smoothed: W4V6 49.5, W16V2 35.7*
+//  quantizer  4608 x 3072: W1V6 8.6*, W4V2 9.1, W8V1 10.1;  smoothed: W2V3 11.3*, W4V2 12.1
+//             4608 x 12288: W4V6 29.2, W8V3 28.2*, W16V2 30.8;  smoothed: W8V3 35.2*, W16V2 38.0
+//             smoothed, 2048 x 6144: W4V3 10.8*, W8V2 11.5;  1024 x 4608: W4V3 7.0*, W8V2 7.9;
+//             512 x 3072: W2V3 4.8, W4V2 4.4*
 //  The norm with 8-bit output keeps reciprocals too: 4608 x 3072 W2V3 28.2, W4V2 25.6.
-constexpr int kNormPerLane = 3, kNormInt8PerLane = 2, kQuantPerLane = 8, kQuantSmoothPerLane = 2;
+constexpr int kNormPerLane = 3, kNormInt8PerLane = 2, kQuantPerLane = 8, kQuantSmoothPerLane = 3;
 
 // Rows per run: one, or with a smoothing vector as many as leave kWavesPerCu
 // waves per compute unit.
@@ -446,10 +448,10 @@ hipError_t launch_quant_int8(const QuantInt8Args& args, hipStream_t stream) {
   a.run = run_for(a.M, w, smooth);
   if (smooth) {
     switch (16 * w + v) {
-      SVDQ_TO2(quant_smooth, 1)
-      SVDQ_TO2(quant_smooth, 2)
-      SVDQ_TO2(quant_smooth, 4)
-      SVDQ_TO2(quant_smooth, 8)
+      SVDQ_TO3(quant_smooth, 1)
+      SVDQ_TO3(quant_smooth, 2)
+      SVDQ_TO3(quant_smooth, 4)
+      SVDQ_TO3(quant_smooth, 8)
       SVDQ_TO8(quant_smooth, 16)
       default: return hipErrorInvalidValue;
     }

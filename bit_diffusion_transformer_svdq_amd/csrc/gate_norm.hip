@@ -25,6 +25,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "row_device.h"
 
 namespace svdq {
@@ -393,11 +395,11 @@ int waves_for(int64_t M, int c8, int per_lane) {
 constexpr int kNormPerLane = 3, kNormInt8PerLane = 2, kQuantPerLane = 8, kQuantSmoothPerLane = 3;
 
 // Rows per run: one, or with a smoothing vector as many as leave kWavesPerCu
-// waves per compute unit.
+// waves per compute unit; more where the launch would come near 2^32 threads, its
+// limit (2^24 rows of 4 waves).
 constexpr int kWavesPerCu = 32;
 int run_for(int64_t M, int w, bool smooth) {
-  if (!smooth) return 1;
-  const int64_t owners = (int64_t)current_cus() * kWavesPerCu / w;
+  const int64_t owners = std::min<int64_t>(smooth ? (int64_t)current_cus() * kWavesPerCu / w : M, (1 << 25) / w);
   return (int)((M + owners - 1) / owners);
 }
 

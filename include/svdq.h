@@ -507,7 +507,9 @@ svdq_status svdq_debug_set_w8a8_plan(int tile, int splits);
  *   z = norm(h) * weight * (1 + scale) + shift         (norm not SVDQ_NORM_NONE)
  *   RMS norm: v / sqrt(mean(v^2) + eps); layer norm: the same of v - mean(v).
  * All in fp32, z from the unrounded h; a vector that is NULL drops out (gate and
- * the weights as 1, scale and shift as 0).  z leaves as bf16, or with
+ * the weights as 1, scale and shift as 0).  A normed row whose sum of squares
+ * passes fp32 (channels of about 1e19) is not defined; other rows are not touched
+ * by it, nor by a row with infinities or NaN.  z leaves as bf16, or with
  * SVDQ_NORM_OUT_INT8 as the codes and token scales that svdq_w8a8_gemm reads:
  * those of svdq_quantize_act_int8 for v = fl32(z fl32(1/smooth)) (or z) in the
  * place of x_hat, not rounded to bf16 in between.

@@ -187,3 +187,25 @@ def test_empty():
     x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
     h, z = P.gate_norm_modulate(x, x)
     assert h.shape == (0, 64) and z.shape == (0, 64)
+
+
+def test_most_rows():
+    """2^24 rows on 4 waves each: more threads than one launch has, so a workgroup
+    takes more than one row.  Every row as in a small call."""
+    import torch
+    import bit_diffusion_transformer_svdq_amd as P
+    M, C, B_ = 1 << 24, 2112, 4096
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 125 << 30:
+        pytest.skip("needs 125 GiB of free device memory")
+    small = torch.randn(B_, C, device="cuda").bfloat16()
+    _, (want, ws) = P.gate_norm_modulate(small, norm="rms", quantize="int8")
+    x = torch.empty(M, C, dtype=torch.bfloat16, device="cuda")
+    x.view(-1, B_, C).copy_(small)
+    _, (q, s) = P.gate_norm_modulate(x, norm="rms", quantize="int8")
+    assert bool((s.view(-1, B_) == ws).all())
+    q = q.view(-1, B_, C)
+    for i in range(0, q.shape[0], 256):
+        assert bool((q[i:i + 256] == want).all()), i
+    del x, q, s
+    torch.cuda.empty_cache()

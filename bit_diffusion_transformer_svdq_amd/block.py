@@ -4,8 +4,8 @@ the gated residual norms and the rotary positions with several axes.
 Like the rest of the binding this module only checks and marshals arguments
 and allocates outputs; the arithmetic is in the library (include/svdq.h).  A call
 runs on the current device's current stream, or on ``stream``: its outputs then
-belong to that stream, and inputs freed meanwhile are kept for it; ordering the
-two streams is the caller's part.  Tensors of another device are refused.
+belong to that stream, and tensors given to it are kept for it if they are freed
+meanwhile; ordering the two streams is the caller's part.  Tensors of another device are refused.
 
 A block's pass, with the modulation vectors from ``awq_w4a16_gemm``::
 
@@ -147,7 +147,7 @@ def quantize_act_int8(x, smooth=None, out=None, stream=None):
         pa = _dense(scales, torch.float32, (M,), idx, "act_scales")
     check(lib().svdq_quantize_act_int8(px, ps, M, K, pc, pa, _raw_stream(idx, stream)), "svdq_quantize_act_int8")
     if stream is not None:
-        _hold(stream, x, smooth)
+        _hold(stream, x, smooth, codes, scales)
     return codes, scales
 
 
@@ -179,7 +179,7 @@ def w8a8_gemm(act_codes, act_scales, w_codes, w_scales, bias=None, out=None, str
         need, act_codes.device, stream, workspace)
     check(L.svdq_w8a8_gemm(pa, ps, pw, pz, pb, M, N, K, epi, py, ws, wsb, _raw_stream(idx, stream)), "svdq_w8a8_gemm")
     if stream is not None:
-        _hold(stream, act_codes, act_scales, w_codes, w_scales, bias)
+        _hold(stream, act_codes, act_scales, w_codes, w_scales, bias, y, workspace)
     return y
 
 
@@ -263,7 +263,7 @@ def gate_norm_modulate(x, y=None, post_norm="none", post_weight=None, gate=None,
         px, int(fp32), xs, py, ys, post, ppw, pg, gr, gs, residual_scale, kind, pw, psc, psh, mr, ms, eps, M, C,
         ph, hs, int(quantize is not None), psm, pz, pzs, _raw_stream(idx, stream)), "svdq_gate_norm_modulate")
     if stream is not None:
-        _hold(stream, x, y, post_weight, gate, weight, scale, shift, smooth)
+        _hold(stream, x, y, post_weight, gate, weight, scale, shift, smooth, h, *(z if isinstance(z, tuple) else (z,)))
     return h, z
 
 
@@ -303,7 +303,7 @@ def rope_axes_tables(positions, axes, theta=10000.0, spectrum="axis", out=None, 
                                       _choice(_SPECTRA, spectrum, "spectrum"), cos.data_ptr(), sin.data_ptr(),
                                       _raw_stream(idx, stream)), "svdq_rope_axes_tables")
     if stream is not None:
-        _hold(stream, positions)
+        _hold(stream, positions, cos, sin)
     return cos, sin
 
 
@@ -344,7 +344,7 @@ def rope_axes(q, k, positions, axes, theta=10000.0, spectrum="axis", layout="pai
         _choice(_SPECTRA, spectrum, "spectrum"), _choice(_LAYOUTS, layout, "layout"), pqn, pkn, eps, pqo, qos, pko,
         kos, _raw_stream(idx, stream)), "svdq_rope_axes")
     if stream is not None:
-        _hold(stream, q, k, positions, q_norm, k_norm)
+        _hold(stream, q, k, positions, q_norm, k_norm, qo, ko)
     return qo, ko
 
 

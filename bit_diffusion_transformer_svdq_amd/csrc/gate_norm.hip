@@ -95,18 +95,18 @@ __global__ __launch_bounds__(threads_of<W>()) void gate_norm_kernel(const GateNo
   const bool live = (V - 1) * 64 * W + lane0 < C8;
 
   // the reciprocals stay in registers over a run, except where a row alone
-  // fills them (16 waves, more than 8192 channels)
+  // fills them (16 waves, more than 8192 channels).  With one vector per lane (few
+  // rows) they are taken behind the first row's loads (64 x 3072 5.1 -> 4.6 us),
+  // with more ahead of the rows (4608 x 3072 25.7 -> 25.0 us)
   constexpr bool kKeep = Q8 && (W < 16 || V == 1);
   float mu[kKeep ? V : 1][8];
-  auto reciprocals = [&](int v, float (&m)[8]) {
-    float sm[8];
-    load_f8(a.smooth + off[v], sm);
-    recip8(sm, m);
-  };
   if constexpr (kKeep) {
     if (a.smooth != nullptr) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) reciprocals(v, mu[v]);
+      for (int v = 0; v < V; ++v) {
+        load_f8(a.smooth + off[v], mu[v]);
+        if constexpr (V > 1) recip8(mu[v]);
+      }
     }
   }
   auto load_all = [&](uint4 (&r)[V], const uint16_t* p, size_t at) {
@@ -253,10 +253,12 @@ __global__ __launch_bounds__(threads_of<W>()) void gate_norm_kernel(const GateNo
         if (a.smooth != nullptr) {
           float m[8];
           if constexpr (kKeep) {
+            if (V == 1 && row == row0) recip8(mu[v]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) m[e] = mu[v][e];
           } else {
-            reciprocals(v, m);
+            load_f8(a.smooth + off[v], m);
+            recip8(m);
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) h[v][e] *= m[e];
@@ -298,14 +300,12 @@ __global__ __launch_bounds__(threads_of<W>()) void quant_int8_kernel(const Quant
   for (int v = 0; v < V; ++v) off[v] = 8 * min(v * 64 * W + lane0, K8 - 1);
   const bool live = (V - 1) * 64 * W + lane0 < K8;
   float mu[kKeep ? V : 1][8];
-  auto reciprocals = [&](int v, float (&m)[8]) {
-    float sm[8];
-    load_f8(a.smooth + off[v], sm);
-    recip8(sm, m);
-  };
   if constexpr (kSmooth && kKeep) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) reciprocals(v, mu[v]);
+    for (int v = 0; v < V; ++v) {
+      load_f8(a.smooth + off[v], mu[v]);
+      if constexpr (V > 1) recip8(mu[v]);  // (V == 1: as in the norm)
+    }
   }
   for (int row = row0; row < row_end; ++row) {
     uint4 p[V];
@@ -319,10 +319,12 @@ __global__ __launch_bounds__(threads_of<W>()) void quant_int8_kernel(const Quant
       if constexpr (kSmooth) {
         float m[8];
         if constexpr (kKeep) {
+          if (V == 1 && row == row0) recip8(mu[v]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) m[e] = mu[v][e];
         } else {
-          reciprocals(v, m);
+          load_f8(a.smooth + off[v], m);
+          recip8(m);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= m[e];

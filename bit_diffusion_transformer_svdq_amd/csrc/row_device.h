@@ -80,10 +80,10 @@ __device__ __forceinline__ float row_reduce(float x, float* lds, int slot) {
   return x;
 }
 
-// fl32(1 / s), correctly rounded.  v_rcp_f32 is within one ulp, and one Newton
-// step with an exact residual then rounds correctly except where every
-// significand bit of s is one (Markstein, 1990); those, and exponents near the
-// ends of the range, take the IEEE division.
+// fl32(1 / s), correctly rounded, in the place of s.  v_rcp_f32 is within one ulp,
+// and one Newton step with an exact residual then rounds correctly except where
+// every significand bit of s is one (Markstein, 1990); those, and exponents near
+// the ends of the range, take the IEEE division.
 __device__ __forceinline__ bool rcp_is_plain(float s) {
   const row_u32 b = __builtin_bit_cast(row_u32, s) & 0x7FFFFFFFu;
   return b >= (27u << 23) && b < (227u << 23) && (b & 0x7FFFFFu) != 0x7FFFFFu;
@@ -92,16 +92,16 @@ __device__ __forceinline__ float rcp_plain(float s) {
   const float r = __builtin_amdgcn_rcpf(s);
   return __builtin_fmaf(__builtin_fmaf(-s, r, 1.0f), r, r);
 }
-__device__ __forceinline__ void recip8(const float (&s)[8], float (&r)[8]) {
+__device__ __forceinline__ void recip8(float (&s)[8]) {
   bool plain = true;
 #pragma unroll
   for (int e = 0; e < 8; ++e) plain = plain && rcp_is_plain(s[e]);
   if (__all(plain)) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = rcp_plain(s[e]);
+    for (int e = 0; e < 8; ++e) s[e] = rcp_plain(s[e]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = 1.0f / s[e];
+    for (int e = 0; e < 8; ++e) s[e] = 1.0f / s[e];
   }
 }
 

@@ -25,11 +25,18 @@
 //    the same in the upper half) over 256 bytes of banks: in each phase the even
 //    and the odd rows then take 8 different slots, no two lanes one bank;
 //  * few tiles: K is split over workgroups, whose int32 partials meet in the
-//    caller's workspace (integer sums: the order does not matter).
+//    caller's workspace (integer sums: the order does not matter);
+//  * many tiles: a workgroup stays and takes one after the other; the last R
+//    stages of a tile fetch the first of the next, and while its Y leaves they
+//    arrive (4608 x 3072 -> 12288 with GELU 165 -> 159 us, 16384 x 4096 -> 4096 221 -> 217).
+//    Y with ordinary instead of streaming stores then takes 232 us of the latter,
+//    and not waiting for the stores before the next tile's second stage 240: the
+//    workgroups of an XCD drift apart and share less of its L2.
 //
 // The MFMA A operand is the weight tile (rows n), B the token tile (columns m),
 // so lane l holds Y[m = l % 16][n = 4 (l / 16) + v] of each 16 x 16 tile; Y leaves
-// through LDS in runs of 64 WI bytes per row.
+// through LDS in runs of 64 WI bytes per row, 16 rows of a wave at a time (all of a
+// wave's rows at once, in the stages' LDS: 1333 x 3072 -> 3072 22.0 us against 19.9).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -96,6 +103,7 @@ __device__ __forceinline__ void tile_of(int bid, int tiles_m, int tiles_n, int& 
 struct TileArgs {
   W8a8Args g;
   int splits;    // over K, gridDim.y
+  int tiles;     // of the whole launch; without splits a workgroup takes every gridDim.x-th
   u32* count;    // one arrival counter per wave sub-tile (splits > 1)
   int* part;     // int32 partials [sub-tile][splits][WI WJ 16][64]
 };
@@ -105,15 +113,21 @@ template <int WI, int WJ, int WN, int WM, int R>
 struct Shape {
   static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves;
   static constexpr int kTN = 32 * WI * WN, kTM = 32 * WJ * WM;
-  static constexpr int kLds = R * 128 * (kTN + kTM);
+  static constexpr int kLds = R * 128 * (kTN + kTM) + kWaves * 1024 * WI;
+  static_assert(kLds <= 160 * 1024, "the stages and the rows of Y on their way fit the LDS");
   static constexpr int kWgs = kLds > 80 * 1024 ? 1 : 2;  // per CU, by LDS
-  static constexpr int kSub = WI * WJ * 1024;                             // accumulators of a wave
+  static constexpr int kSub = WI * WJ * 1024;            // accumulators of a wave
 };
 
-template <int WI, int WJ, int WN, int WM, int R, bool kSplit>
+// kOne: a tile per workgroup; kSplits: the same over a part of K; kMany: several tiles
+// per workgroup, one after the other, all of them whole, K % (128 R) == 0
+enum Mode { kOne, kSplits, kMany };
+
+template <int WI, int WJ, int WN, int WM, int R, Mode kMode>
 __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_tile_kernel(const TileArgs p) {
   using Sh = Shape<WI, WJ, WN, WM, R>;
   static_assert(R >= 2 && R <= 4, "stage buffers");
+  constexpr bool kSplit = kMode == kSplits, kWhole = kMode == kMany;
   constexpr int kTN = Sh::kTN, kTM = Sh::kTM, kWaves = Sh::kWaves;
   // one LDS object per operand and stage, so the compiler sees that a DMA
   // into one cannot alias reads of another
@@ -123,11 +137,11 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
   auto wbuf = [&](int b) -> uint8_t* { return b == 0 ? w0 : b == 1 ? w1 : b == 2 ? w2 : w3; };
   auto abuf = [&](int b) -> uint8_t* { return b == 0 ? a0 : b == 1 ? a1 : b == 2 ? a2 : a3; };
 
+  // the epilogue's own: 16 rows of each wave's sub-tile
+  __shared__ __attribute__((aligned(16))) uint8_t rows[kWaves * 1024 * WI];
+
   const int M = p.g.M, N = p.g.N, K = p.g.K;
-  int tm, tn;
-  tile_of(blockIdx.x, (M + kTM - 1) / kTM, (N + kTN - 1) / kTN, tm, tn);
-  const int n0 = tn * kTN;
-  const int m0 = tm * kTM;
+  const int tiles_n = (N + kTN - 1) / kTN;
   // stages of 128 k; the last one may be half (K % 128 == 64)
   const int S_all = (K + 127) >> 7;
   const int q_begin = kSplit ? (int)((long)blockIdx.y * S_all / p.splits) : 0;
@@ -147,22 +161,35 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
   // lane % 8 of each row, with granule (lane % 8) ^ row[3:1].  Rows past the
   // end repeat the last row (never stored).  In a half stage the granules of
   // the missing half repeat those of the first.
-  const uint8_t* wbase = reinterpret_cast<const uint8_t*>(p.g.w) + (size_t)n0 * (size_t)K;
-  const uint8_t* abase = reinterpret_cast<const uint8_t*>(p.g.act) + (size_t)m0 * (size_t)K;
   const u32 gran = 16u * (u32)((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));
-  const u32 back = (K & 64) != 0 && gran >= 64 ? 64u : 0u;
+  const u32 back = !kWhole && (K & 64) != 0 && gran >= 64 ? 64u : 0u;
   constexpr int kWd = kTN / (8 * kWaves), kAd = kTM / (8 * kWaves);  // DMAs per stage and wave
   static_assert(kWaves % 2 == 0 && kWd * 8 * kWaves == kTN && kAd * 8 * kWaves == kTM, "whole row runs per wave");
-  // (N % 64 == 0: the 8 weight rows of an instruction are all inside or all
-  // past the end, so their offset is uniform)
-  u32 woff[kWd], aoff[kAd];
   const u32 wlane = (u32)(lane >> 3) * (u32)K + gran;
+  const uint8_t *wbase, *abase;
+  u32 woff[kWd], aoff[kAd];
+  // the tile that the DMAs fill (one or more stages ahead of the products)
+  int n0, m0;
+  auto dma_tile = [&](int t) {
+    int tm, tn;
+    tile_of(t, (M + kTM - 1) / kTM, tiles_n, tm, tn);
+    n0 = tn * kTN, m0 = tm * kTM;
+    wbase = reinterpret_cast<const uint8_t*>(p.g.w) + (size_t)n0 * (size_t)K;
+    abase = reinterpret_cast<const uint8_t*>(p.g.act) + (size_t)m0 * (size_t)K;
+    // (N % 64 == 0: the 8 weight rows of an instruction are all inside or all
+    // past the end, so their offset is uniform)
 #pragma unroll
-  for (int k = 0; k < kWd; ++k)
-    woff[k] = (u32)__builtin_amdgcn_readfirstlane(min(n0 + 8 * (kWaves * k + wave), N - 8) - n0) * (u32)K;
+    for (int k = 0; k < kWd; ++k) {
+      const int row = 8 * (kWaves * k + wave);
+      woff[k] = (u32)(kWhole ? row : __builtin_amdgcn_readfirstlane(min(n0 + row, N - 8) - n0)) * (u32)K;
+    }
 #pragma unroll
-  for (int k = 0; k < kAd; ++k)
-    aoff[k] = (u32)(min(m0 + 8 * (kWaves * k + wave) + (lane >> 3), M - 1) - m0) * (u32)K + gran;
+    for (int k = 0; k < kAd; ++k) {
+      const int row = 8 * (kWaves * k + wave);
+      if constexpr (kWhole) aoff[k] = (u32)row * (u32)K;
+      else aoff[k] = (u32)(min(m0 + row + (lane >> 3), M - 1) - m0) * (u32)K + gran;
+    }
+  };
   // column of stage q (counted from q_begin; past the end the last stage again), and
   // how far back the lane's granule lies in it
   auto stage_col = [&](int q) {
@@ -170,25 +197,23 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
     return u32x2{128u * (u32)s, s == S_all - 1 ? back : 0u};
   };
   constexpr int kDmas = kWd + kAd;
-  auto dma_one = [&](int k, u32x2 col, auto bc) {
+  auto dma_one = [&](int k, u32x2 col, u32 wlane, auto bc) {
     constexpr int b = decltype(bc)::value;
-    if (k < kWd)
-      dma16(wbase + (woff[k] + col.x) + (wlane - col.y), wbuf(b) + 1024 * (kWaves * k + wave));
-    else
-      dma16(abase + col.x + (aoff[k - kWd] - col.y), abuf(b) + 1024 * (kWaves * (k - kWd) + wave));
+    const int ka = k - kWd;
+    if (k < kWd) dma16(wbase + (woff[k] + col.x) + (wlane - col.y), wbuf(b) + 1024 * (kWaves * k + wave));
+    else if constexpr (kWhole) dma16(abase + (aoff[ka] + col.x) + wlane, abuf(b) + 1024 * (kWaves * ka + wave));
+    else dma16(abase + col.x + (aoff[ka] - col.y), abuf(b) + 1024 * (kWaves * ka + wave));
   };
   auto dma_stage = [&](int q, auto bc) {
     const u32x2 col = stage_col(q);
 #pragma unroll
-    for (int k = 0; k < kDmas; ++k) dma_one(k, col, bc);
+    for (int k = 0; k < kDmas; ++k) dma_one(k, col, wlane, bc);
   };
 
   // Fragment reads: lane (l16, lq) takes granule 4 hh + lq of rows 16 i + l16 for
   // half hh, a k step of 64.
   constexpr int kI = 2 * WI, kJ = 2 * WJ;  // 16 x 16 tiles of a wave
-  int fo[2];
-#pragma unroll
-  for (int hh = 0; hh < 2; ++hh) fo[hh] = 128 * l16 + 16 * ((4 * hh + lq) ^ (l16 >> 1));
+  const int fo = 128 * l16 + 16 * (lq ^ (l16 >> 1));
   const int wrow = wn * 32 * WI * 128, arow = wm * 32 * WJ * 128;
   struct Frags {
     v4i w[kI], a[kJ];
@@ -197,17 +222,16 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
     constexpr int b = decltype(bc)::value, hh = decltype(hc)::value;
     const uint8_t* wt = wbuf(b) + wrow;
     const uint8_t* at = abuf(b) + arow;
+    int at0 = fo;
+    __asm__ volatile("" : "+v"(at0));  // no register per buffer and half
+    at0 ^= 64 * hh;
 #pragma unroll
-    for (int i = 0; i < kI; ++i) f.w[i] = *reinterpret_cast<const v4i*>(wt + fo[hh] + 2048 * i);
+    for (int i = 0; i < kI; ++i) f.w[i] = *reinterpret_cast<const v4i*>(wt + at0 + 2048 * i);
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) f.a[j] = *reinterpret_cast<const v4i*>(at + fo[hh] + 2048 * j);
+    for (int j = 0; j < kJ; ++j) f.a[j] = *reinterpret_cast<const v4i*>(at + at0 + 2048 * j);
   };
 
   v4i acc[kI][kJ];
-#pragma unroll
-  for (int i = 0; i < kI; ++i)
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
   auto mfma_half = [&](const Frags& f) {
 #pragma unroll
     for (int i = 0; i < kI; ++i)
@@ -238,13 +262,7 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
   using B2 = std::integral_constant<int, 2>;
   using B3 = std::integral_constant<int, 3>;
   Frags f0, f1;
-  dma_stage(0, B0{});
-  dma_stage(1, B1{});
-  if constexpr (R > 2) dma_stage(2, B2{});
-  if constexpr (R > 3) dma_stage(3, B3{});
-  wait_vm_lds<(R - 1) * kDmas>();
-  barrier();
-  read_half(f0, B0{}, B0{});
+  int shift = 0;  // stages by which the DMAs run ahead into the next tile
   auto iteration = [&](int q, auto bc) {
     constexpr int b = decltype(bc)::value;
     using BC = std::integral_constant<int, b>;
@@ -253,129 +271,161 @@ __global__ __launch_bounds__((Shape<WI, WJ, WN, WM, R>::kThreads), 2) void w8a8_
     read_half(f1, BC{}, B1{});
     mfma_half(f0);
     interleave(B0{});
-    const u32x2 col = stage_col(q + R);
+    const u32x2 col = stage_col(q + R + shift);
     // this wave's reads of the stage, and its DMAs of the next one; those of
     // the R - 2 stages after it may still be in flight
     wait_vm_lds<(R - 2) * kDmas>();
     barrier();
     __builtin_amdgcn_sched_barrier(0);
     read_half(f0, BN{}, B0{});
+    u32 wl = wlane;
+    if constexpr (kWhole) __asm__ volatile("" : "+v"(wl));  // a 32-bit offset to a uniform address
 #pragma unroll
-    for (int k = 0; k < kDmas; ++k) dma_one(k, col, bc);
+    for (int k = 0; k < kDmas; ++k) dma_one(k, col, wl, bc);
     mfma_half(f1);
     interleave(B1{});
   };
-  int q = 0;
-  for (; q + R <= S; q += R) {
-    iteration(q, B0{});
-    iteration(q + 1, B1{});
-    if constexpr (R > 2) iteration(q + 2, B2{});
-    if constexpr (R > 3) iteration(q + 3, B3{});
-  }
-  if (q < S) iteration(q, B0{});
-  if constexpr (R > 2)
-    if (q + 1 < S) iteration(q + 1, B1{});
-  if constexpr (R > 3)
-    if (q + 2 < S) iteration(q + 2, B2{});
-  if (half_end) mfma_half(f0);
-  wait_vm_lds<0>();  // no LDS write may land after this
-  barrier();         // every wave has finished its last LDS reads
-
-  if constexpr (kSplit) {
-    // Each wave stores its int32 sub-tile with agent-coherent stores, waits
-    // for them and bumps the sub-tile's counter (which wraps to zero); the
-    // last to arrive adds the others' and runs the epilogue.
-    constexpr int kSub = Sh::kSub;
-    const size_t sub = ((size_t)tm * ((N + kTN - 1) / kTN) + tn) * kWaves + wave;
-    int* mine = p.part + (sub * p.splits + blockIdx.y) * kSub + lane;
+  int tile = blockIdx.x;
+  dma_tile(tile);
+  dma_stage(0, B0{});
+  dma_stage(1, B1{});
+  if constexpr (R > 2) dma_stage(2, B2{});
+  if constexpr (R > 3) dma_stage(3, B3{});
+  wait_vm_lds<(R - 1) * kDmas>();
+  barrier();
+  for (;;) {
+    read_half(f0, B0{}, B0{});
 #pragma unroll
     for (int i = 0; i < kI; ++i)
 #pragma unroll
-      for (int j = 0; j < kJ; ++j)
+      for (int j = 0; j < kJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+    const int tn0 = n0, tm0 = m0;  // of the products
+    const int next = tile + (int)gridDim.x;
+    const bool more = kWhole && next < p.tiles;
+    shift = 0;
+    int q = 0;
+    for (; q + R <= S; q += R) {
+      // the last R stages fetch the first of the next tile
+      if (more && q + R == S) {
+        dma_tile(next);
+        shift = -S;
+      }
+      iteration(q, B0{});
+      iteration(q + 1, B1{});
+      if constexpr (R > 2) iteration(q + 2, B2{});
+      if constexpr (R > 3) iteration(q + 3, B3{});
+    }
+    if constexpr (!kWhole) {
+      if (q < S) iteration(q, B0{});
+      if constexpr (R > 2)
+        if (q + 1 < S) iteration(q + 1, B1{});
+      if constexpr (R > 3)
+        if (q + 2 < S) iteration(q + 2, B2{});
+      if (half_end) mfma_half(f0);
+    }
+
+    if constexpr (kSplit) {
+      // Each wave stores its int32 sub-tile with agent-coherent stores, waits
+      // for them and bumps the sub-tile's counter (which wraps to zero); the
+      // last to arrive adds the others' and runs the epilogue.
+      constexpr int kSub = Sh::kSub;
+      const size_t sub = (size_t)tile * kWaves + wave;
+      int* mine = p.part + (sub * p.splits + blockIdx.y) * kSub + lane;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          __hip_atomic_store(mine + (((i * kJ + j) * 4 + e) << 6), acc[i][j][e], __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
-    __asm__ volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): the partial is visible to the agent
-    __asm__ volatile("" ::: "memory");
-    u32 old = 0;
-    if (lane == 0) old = atomicInc(p.count + sub, (u32)(p.splits - 1));
-    old = __shfl(old, 0);
-    if (old != (u32)(p.splits - 1)) return;
-    __asm__ volatile("" ::: "memory");
-    for (int s = 0; s < p.splits; ++s) {
-      if (s == (int)blockIdx.y) continue;
-      const int* src = p.part + (sub * p.splits + s) * kSub + lane;
-#pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        v4i t[kJ];
+      for (int i = 0; i < kI; ++i)
 #pragma unroll
         for (int j = 0; j < kJ; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            t[j][e] = __hip_atomic_load(src + (((i * kJ + j) * 4 + e) << 6), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(mine + (((i * kJ + j) * 4 + e) << 6), acc[i][j][e], __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+      __asm__ volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): the partial is visible to the agent
+      __asm__ volatile("" ::: "memory");
+      u32 old = 0;
+      if (lane == 0) old = atomicInc(p.count + sub, (u32)(p.splits - 1));
+      old = __shfl(old, 0);
+      if (old != (u32)(p.splits - 1)) break;
+      __asm__ volatile("" ::: "memory");
+      for (int s = 0; s < p.splits; ++s) {
+        if (s == (int)blockIdx.y) continue;
+        const int* src = p.part + (sub * p.splits + s) * kSub + lane;
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) acc[i][j] += t[j];
+        for (int i = 0; i < kI; ++i) {
+          v4i t[kJ];
+#pragma unroll
+          for (int j = 0; j < kJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              t[j][e] = __hip_atomic_load(src + (((i * kJ + j) * 4 + e) << 6), __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) acc[i][j] += t[j];
+        }
       }
     }
-  }
 
-  // y = bf16(epi(acc fl32(s_x s_w) + b)) in fp32 (int32 -> fp32 rounds to 24
-  // bits, far below the bf16 rounding).  The wave writes its 32 WJ x 32 WI
-  // sub-tile to LDS (the stages are free) as rows m of 64 WI bytes, and stores
-  // it from there in row runs.
-  constexpr int kChunks = 4 * WI;                    // 16-byte chunks of a sub-tile row
-  constexpr int kMask = kChunks % 8 == 0 ? 7 : 3;    // chunk c of row m sits at c ^ (m & kMask)
-  constexpr int kPerBuf = kWaves / 4;                // waves that share a stage buffer
-  static_assert(kPerBuf * 2 * Sh::kSub <= 128 * (kTN < kTM ? kTN : kTM), "sub-tiles fit the stages");
-  const int sb = wave / kPerBuf;
-  uint8_t* stage = (sb == 0 ? w0 : sb == 1 ? w1 : sb == 2 ? a0 : a1) + (wave % kPerBuf) * 2 * Sh::kSub;
-  const int nw = n0 + wn * 32 * WI, mw = m0 + wm * 32 * WJ;  // the wave's first column and row
-  float sx[kJ];
+    // y = bf16(epi(acc fl32(s_x s_w) + b)) in fp32 (int32 -> fp32 rounds to 24
+    // bits, far below the bf16 rounding).  The wave turns its sub-tile 16 token rows
+    // at a time through LDS of its own, so that Y leaves in row runs of 64 WI bytes.
+    constexpr int kChunks = 4 * WI;                    // 16-byte chunks of a sub-tile row
+    constexpr int kMask = kChunks % 8 == 0 ? 7 : 3;    // chunk c of row m sits at c ^ (m & kMask)
+    // (the lane number anew: what the epilogue derives from it is not worth
+    // registers during the products)
+    int el = lane;
+    __asm__ volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(el));
+    const int e16 = el & 15, eq = el >> 4;
+    uint8_t* turn = rows + wave * 1024 * WI;
+    const int nw = tn0 + wn * 32 * WI, mw = tm0 + wm * 32 * WJ;  // the wave's first column and row
+    float sx[kJ];
+    float4 sw[kI];
+    uint2 b2[kI];
 #pragma unroll
-  for (int j = 0; j < kJ; ++j) sx[j] = p.g.act_scales[min(mw + 16 * j + l16, M - 1)];
+    for (int j = 0; j < kJ; ++j) sx[j] = p.g.act_scales[kWhole ? mw + 16 * j + e16 : min(mw + 16 * j + e16, M - 1)];
 #pragma unroll
-  for (int i = 0; i < kI; ++i) {
-    const int nl = 16 * i + 4 * lq;  // within the wave's columns
-    const int nc = min(nw + nl, N - 4);
-    const float4 sw = *reinterpret_cast<const float4*>(p.g.w_scales + nc);
-    float bb[4] = {0.f, 0.f, 0.f, 0.f};
-    if (p.g.bias != nullptr) {
-      const uint2 b2 = *reinterpret_cast<const uint2*>(p.g.bias + nc);
-      bb[0] = bf16_lo(b2.x), bb[1] = bf16_hi(b2.x), bb[2] = bf16_lo(b2.y), bb[3] = bf16_hi(b2.y);
+    for (int i = 0; i < kI; ++i) {
+      const int nc = kWhole ? nw + 16 * i + 4 * eq : min(nw + 16 * i + 4 * eq, N - 4);
+      sw[i] = *reinterpret_cast<const float4*>(p.g.w_scales + nc);
+      b2[i] = p.g.bias != nullptr ? *reinterpret_cast<const uint2*>(p.g.bias + nc) : uint2{0u, 0u};
     }
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
-      float o[4];
-      o[0] = __builtin_fmaf((float)acc[i][j][0], sx[j] * sw.x, bb[0]);
-      o[1] = __builtin_fmaf((float)acc[i][j][1], sx[j] * sw.y, bb[1]);
-      o[2] = __builtin_fmaf((float)acc[i][j][2], sx[j] * sw.z, bb[2]);
-      o[3] = __builtin_fmaf((float)acc[i][j][3], sx[j] * sw.w, bb[3]);
-      if (p.g.epilogue == kEpilogueGelu) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) o[v] = gelu_exp2(o[v]);
+      for (int i = 0; i < kI; ++i) {
+        float o[4];
+        o[0] = __builtin_fmaf((float)acc[i][j][0], sx[j] * sw[i].x, bf16_lo(b2[i].x));
+        o[1] = __builtin_fmaf((float)acc[i][j][1], sx[j] * sw[i].y, bf16_hi(b2[i].x));
+        o[2] = __builtin_fmaf((float)acc[i][j][2], sx[j] * sw[i].z, bf16_lo(b2[i].y));
+        o[3] = __builtin_fmaf((float)acc[i][j][3], sx[j] * sw[i].w, bf16_hi(b2[i].y));
+        if (p.g.epilogue == kEpilogueGelu) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) o[v] = gelu_exp2(o[v]);
+        }
+        const int nl = 16 * i + 4 * eq;  // within the wave's columns
+        uint8_t* dst = turn + e16 * (16 * kChunks) + (((nl >> 3) ^ (e16 & kMask)) << 4) + 8 * (eq & 1);
+        *reinterpret_cast<uint2*>(dst) = uint2{pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3])};
       }
-      const int ml = 16 * j + l16;
-      uint8_t* dst = stage + ml * (16 * kChunks) + (((nl >> 3) ^ (ml & kMask)) << 4) + 8 * (lq & 1);
-      *reinterpret_cast<uint2*>(dst) = uint2{pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3])};
-    }
-  }
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes are done
-  __asm__ volatile("" ::: "memory");
-  // chunk by chunk in row order: an instruction stores 64 chunks, whole rows of
-  // 64 WI bytes where they divide 64
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes are done
+      __asm__ volatile("" ::: "memory");
+      // chunk by chunk in row order: an instruction stores 64 chunks, whole rows of
+      // 64 WI bytes where they divide 64
 #pragma unroll
-  for (int t = 0; t < 32 * WJ * kChunks / 64; ++t) {
-    const int at = 64 * t + lane;
-    const int ml = at / kChunks, c = at - ml * kChunks;
-    const int m = mw + ml, n = nw + 8 * c;
-    const uint4 v = *reinterpret_cast<const uint4*>(stage + ml * (16 * kChunks) + ((c ^ (ml & kMask)) << 4));
-    // streaming (non-temporal) stores: Y is not read again by this launch;
-    // N % 64 == 0, so n < N covers n + 7
-    if (m < M && n < N)
-      __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p.g.y + (size_t)m * N + n));
+      for (int t = 0; t < WI; ++t) {
+        const int at = 64 * t + el;
+        const int ml = at / kChunks, c = at - ml * kChunks;
+        const int m = mw + 16 * j + ml, n = nw + 8 * c;
+        const uint4 v = *reinterpret_cast<const uint4*>(turn + ml * (16 * kChunks) + ((c ^ (ml & kMask)) << 4));
+        // streaming (non-temporal) stores: Y is not read again by this launch;
+        // N % 64 == 0, so n < N covers n + 7
+        if (kWhole || (m < M && n < N))
+          __builtin_nontemporal_store(v4u{v.x, v.y, v.z, v.w}, reinterpret_cast<v4u*>(p.g.y + (size_t)m * N + n));
+      }
+      __asm__ volatile("" ::: "memory");  // (a wave's LDS operations run in order)
+    }
+    if (!more) break;
+    tile = next;
   }
+  wait_vm_lds<0>();  // no DMA may land after the workgroup's end
 }
 
 struct Plan {
@@ -390,17 +440,17 @@ struct Plan {
 // compute unit, base + n (fill + S step) us for S stages of 128 k; where two
 // workgroups share a compute unit, base + (n / 2) (fill2 + S step2), an odd one
 // at fill and step.  Fitted to 80 shapes (65 to 4608 tokens, K 512 to 12288, N 256
-// to 12288) on MI355X, every tile and split timed: the plan's pick is within 0.7 %
-// (geometric mean) of the best measured one, 11 % at most.
+// to 12288) on MI355X, every tile and split timed: the plan's pick is within 0.3 %
+// (geometric mean) of the best measured one, 6 % at most.
 #define SVDQ_SHAPES(X)                                   \
-  X(442, 4, 2, 2, 4, 2, -4.89, 13.11, 1.107, 0.0, 0.0)   \
-  X(342, 3, 2, 2, 4, 2, -4.51, 11.32, 0.940, 0.0, 0.0)   \
-  X(432, 2, 3, 4, 2, 2, -3.25, 9.60, 0.936, 0.0, 0.0)    \
-  X(323, 3, 2, 2, 2, 3, 0.26, 6.76, 0.565, 0.0, 0.0)     \
-  X(224, 2, 2, 2, 2, 4, 1.08, 5.02, 0.380, 0.0, 0.0)     \
-  X(222, 2, 2, 2, 2, 2, 0.39, 4.13, 0.618, 5.95, 0.756)  \
-  X(124, 1, 2, 2, 2, 4, 2.03, 2.69, 0.259, 0.0, 0.0)     \
-  X(114, 1, 1, 2, 2, 4, 3.12, 1.31, 0.163, 2.02, 0.360)
+  X(442, 4, 2, 2, 4, 2, -3.29, 11.18, 1.109, 0.0, 0.0)   \
+  X(342, 3, 2, 2, 4, 2, -2.66, 9.36, 0.937, 0.0, 0.0)    \
+  X(432, 2, 3, 4, 2, 2, -1.86, 8.15, 0.941, 0.0, 0.0)    \
+  X(323, 3, 2, 2, 2, 3, 0.14, 6.64, 0.507, 0.0, 0.0)     \
+  X(224, 2, 2, 2, 2, 4, 1.06, 4.89, 0.372, 0.0, 0.0)     \
+  X(222, 2, 2, 2, 2, 2, 0.66, 3.67, 0.619, 5.38, 0.788)  \
+  X(124, 1, 2, 2, 2, 4, 2.08, 2.83, 0.260, 0.0, 0.0)     \
+  X(114, 1, 1, 2, 2, 4, 3.00, 1.45, 0.175, 2.07, 0.365)
 struct ShapeInfo {
   int code, tn, tm, waves, wgs, sub;
   double base, fill, step, fill2, step2;
@@ -441,7 +491,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
       } else {
         cost += n * (s.fill + S * s.step);
       }
-      if (splits > 1) cost += 2.65 + 0.53 * splits + 0.58 * (s.tn / 64) * (s.tm / 64);  // the partials' round trips
+      if (splits > 1) cost += 2.54 + 0.52 * splits + 0.57 * (s.tn / 64) * (s.tm / 64);  // the partials' round trips
       if (best.shape < 0 || cost < best.cost || (forced > 0 && best.shape == i)) best = Plan{i, (int)tiles, splits, cost};
     }
   }
@@ -451,8 +501,11 @@ Plan plan_of(int64_t M, int64_t N, int64_t K) {
 // The launches of a product: the tokens [0, m1) in whole rounds of one of the
 // largest tiles, and the rest on the tile that suits it (m1 = M: one launch).  The
 // last round of a large tile otherwise leaves most compute units idle (4608 tokens,
-// 3072 -> 12288: 864 tiles of 256 x 256 are 3.4 rounds; 768 and then 256 of 192 x 128 are 4
-// full ones, the last of them a short one).
+// 3072 -> 12288: 864 tiles of 256 x 256 are 3.4 rounds, 156 us; 768 and then 256 of 192 x 128
+// are 4 full ones, the last of them a short one, 150 us).
+// kSecondLaunch: what a second launch takes beyond the model's sum, in us (of 15
+// shapes where the two come close, 3 then run longer than the other choice, by 5 % at most).
+constexpr double kSecondLaunch = 6.5;
 struct Launches {
   int64_t m1;
   Plan first, rest;
@@ -469,7 +522,7 @@ Launches launches_of(int64_t M, int64_t N, int64_t K) {
     const int64_t rounds = nt * mt / cus, mt1 = rounds * cus / nt;
     if (nt * mt > (1 << 30) || mt1 <= 0 || mt1 * s.tm >= M) continue;
     Launches l{mt1 * s.tm, Plan{i, (int)(mt1 * nt), 1, 0.0}, plan_of(M - mt1 * s.tm, N, K)};
-    l.first.cost = s.base + (double)((mt1 * nt + cus - 1) / cus) * (s.fill + S * s.step);
+    l.first.cost = kSecondLaunch + s.base + (double)((mt1 * nt + cus - 1) / cus) * (s.fill + S * s.step);
     if (l.first.cost + l.rest.cost < best_cost) {
       best = l;
       best_cost = l.first.cost + l.rest.cost;
@@ -480,11 +533,21 @@ Launches launches_of(int64_t M, int64_t N, int64_t K) {
 
 template <int WI, int WJ, int WN, int WM, int R>
 void tile_go(const TileArgs& t, int tiles, hipStream_t stream) {
-  const dim3 block(Shape<WI, WJ, WN, WM, R>::kThreads);
+  using Sh = Shape<WI, WJ, WN, WM, R>;
+  const dim3 block(Sh::kThreads);
+  // whole tiles, more than the chip holds at once: one workgroup per compute unit
+  // (of the large tiles, which the plan takes for such products)
+  if constexpr (Sh::kWaves == 8) {
+    const int cus = current_cus();
+    if (t.splits == 1 && tiles > cus && t.g.M % Sh::kTM == 0 && t.g.N % Sh::kTN == 0 && t.g.K % (128 * R) == 0) {
+      hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, WN, WM, R, kMany>), dim3(cus), block, 0, stream, t);
+      return;
+    }
+  }
   if (t.splits > 1)
-    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, WN, WM, R, true>), dim3(tiles, t.splits), block, 0, stream, t);
+    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, WN, WM, R, kSplits>), dim3(tiles, t.splits), block, 0, stream, t);
   else
-    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, WN, WM, R, false>), dim3(tiles), block, 0, stream, t);
+    hipLaunchKernelGGL((w8a8_tile_kernel<WI, WJ, WN, WM, R, kOne>), dim3(tiles), block, 0, stream, t);
 }
 
 }  // namespace
@@ -524,7 +587,7 @@ size_t w8a8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 
 static hipError_t launch_plan(const W8a8Args& a, const Plan& p, const Workspace& ws, hipStream_t stream) {
   if (plan_bytes(p) > ws.bytes) return hipErrorInvalidValue;
-  TileArgs t{a, p.splits, nullptr, nullptr};
+  TileArgs t{a, p.splits, p.tiles, nullptr, nullptr};
   if (p.splits > 1) {
     t.count = ws_counters(ws);
     t.part = static_cast<int*>(ws_scratch(ws));

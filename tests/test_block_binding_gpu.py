@@ -237,3 +237,25 @@ def test_whole_rounds_and_the_rest(M, N, K, epilogue):
         want = _plain(c[0][rows], c[1][rows], c[2], c[3]) + b.double()
         err = (2.0 ** -8 + 2.0 ** -20) * want.abs() + 2.0 ** -22 * (want - b.double()).abs()
         assert bool(((y[rows].double() - want).abs() <= err).all())
+
+
+@pytest.mark.parametrize("tile,M,N,K", [(442, 1024, 16640, 256), (442, 256, 65792, 512), (442, 256, 131328, 256),
+                                        (342, 1536, 10752, 768), (432, 4032, 6656, 256), (432, 384, 65536, 1024),
+                                        (442, 1025, 16640, 256), (442, 1024, 16640, 320), (442, 1024, 16576, 384)])
+def test_many_tiles_per_workgroup(tile, M, N, K):
+    """Whole tiles, more of them than compute units and by one or two only: a
+    workgroup's first and last tile come out as in a launch of small tiles; and what
+    is not whole (rows, channels, stages)."""
+    import torch
+    import bit_diffusion_transformer_svdq_amd as P
+    c = _codes(M, N, K, 9)
+    b = torch.randn(N, device="cuda").bfloat16()
+    got = []
+    for t in (tile, 124):
+        P.debug_set_w8a8_plan(t, 1)
+        try:
+            got.append([P.w8a8_gemm(*c, b, epilogue=e) for e in ("none", "gelu_tanh")])
+        finally:
+            P.debug_set_w8a8_plan()
+    for y, w in zip(*got):
+        assert torch.equal(y, w)

@@ -11,10 +11,11 @@
 // "Quantisierung von Modellen mit strukturellen Umschreibungen"); the kernel
 // here turns the Q and K of any other projection.
 //
-// Angles: the rates arrive in revolutions per unit of position, as doubles;
-// the product with the position and its reduction to [-1/2, 1/2] are done in
-// double (three operations per angle), so a far position keeps the 2^-24 of a
-// near one, and sincospif needs no reduction of its own.
+// Angles: the rates arrive in quarter turns per unit of position, as doubles;
+// the product with the position, its reduction to [-1/2, 1/2] quarter turns and the
+// Taylor series of sine and cosine (to t^13 and t^14: below 2^-45 at pi/4) are done in
+// double, about 20 operations per angle, so that a far position keeps the 2^-24 of a
+// near one and each value is rounded once.
 //
 // The turn is bound by HBM: Q and K are read and written once.  A workgroup
 // computes the angles of its tokens once, in LDS, for all their heads, while the
@@ -37,7 +38,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;  // per workgroup; with 8192 heads 2^15 items
 
 struct Rates {
-  double per_unit[kRopeMaxAngles];  // revolutions per unit of position
+  double per_unit[kRopeMaxAngles];  // quarter turns per unit of position
   uint8_t axis[kRopeMaxAngles];
 };
 
@@ -61,11 +62,27 @@ struct TableArgs {
 __device__ __forceinline__ float2 angle_of(const void* positions, int pos_int, int64_t at, double rate) {
   const double p = pos_int ? (double)static_cast<const int32_t*>(positions)[at]
                            : (double)static_cast<const float*>(positions)[at];
-  const double rev = p * rate;
-  const float r = (float)(rev - __builtin_rint(rev));
-  float s, c;
-  sincospif(2.0f * r, &s, &c);
-  return float2{c, s};
+  const double turns = p * rate, quarter = __builtin_rint(turns);
+  const double t = (turns - quarter) * 1.5707963267948966, t2 = t * t;
+  double s = 1.0 / 6227020800.0, c = -1.0 / 87178291200.0;
+  s = __builtin_fma(s, t2, -1.0 / 39916800.0);
+  s = __builtin_fma(s, t2, 1.0 / 362880.0);
+  s = __builtin_fma(s, t2, -1.0 / 5040.0);
+  s = __builtin_fma(s, t2, 1.0 / 120.0);
+  s = __builtin_fma(s, t2, -1.0 / 6.0);
+  s = __builtin_fma(s * t2, t, t);
+  c = __builtin_fma(c, t2, 1.0 / 479001600.0);
+  c = __builtin_fma(c, t2, -1.0 / 3628800.0);
+  c = __builtin_fma(c, t2, 1.0 / 40320.0);
+  c = __builtin_fma(c, t2, -1.0 / 720.0);
+  c = __builtin_fma(c, t2, 1.0 / 24.0);
+  c = __builtin_fma(c, t2, -0.5);
+  c = __builtin_fma(c, t2, 1.0);
+  // the quarter within its turn (exact; NaN stays NaN in s and c)
+  const int k = (int)(quarter - 4.0 * __builtin_floor(quarter * 0.25));
+  const float fs = (float)s, fc = (float)c;
+  const float x = (k & 1) != 0 ? fs : fc, y = (k & 1) != 0 ? fc : fs;
+  return float2{k == 1 || k == 2 ? -x : x, (k & 2) != 0 ? -y : y};
 }
 
 __global__ __launch_bounds__(kThreads) void rope_tables_kernel(const TableArgs a) {
@@ -267,19 +284,19 @@ __global__ __launch_bounds__(kThreads) void rope_turn_kernel(const TurnArgs t) {
   }
 }
 
-// rate of angle i in revolutions: theta^(-2j/d) / (2 pi), j and d within the
-// axis, or theta^(-2i/R) / (2 pi).  A running product in extended precision
+// rate of angle i in quarter turns: theta^(-2j/d) / (pi/2), j and d within the
+// axis, or theta^(-2i/R) / (pi/2).  A running product in extended precision
 // (error below 2^-56 over 128 steps).
 void make_rates(const RopeAxes& x, Rates& f) {
-  const long double turn = 6.283185307179586476925286766559L;
+  const long double quarter = 1.5707963267948966192313216916398L;
   const long double lt = std::log((long double)x.theta);
   int at = 0;
-  long double all = 1.0L / turn;
+  long double all = 1.0L / quarter;
   const long double all_step = std::exp(-lt / (long double)x.half);
   for (int ax = 0; ax < x.n; ++ax) {
     const int pairs = x.width[ax] / 2;
     const long double step = pairs > 0 ? std::exp(-lt / (long double)pairs) : 1.0L;
-    long double v = 1.0L / turn;
+    long double v = 1.0L / quarter;
     for (int j = 0; j < pairs; ++j, ++at) {
       f.per_unit[at] = (double)(x.shared ? all : v);
       f.axis[at] = (uint8_t)ax;

@@ -549,8 +549,8 @@ svdq_status svdq_gate_norm_modulate(
  *   angle_i = position[axis of i] * rate_i,   i = 0 .. R/2 - 1, axis by axis
  *   rate_i  = theta^(-2 j / axes[a])  for the j-th angle of axis a (SVDQ_SPECTRUM_AXIS)
  *           = theta^(-2 i / R)                                     (SVDQ_SPECTRUM_SHARED)
- * The product and its reduction are done in double, so far positions keep
- * their precision.
+ * The product, its reduction and the sine and cosine are done in double, so far
+ * positions keep their precision and each value is rounded to fp32 once.
  *
  * svdq_rope_axes_tables writes cos and sin, fp32 [M, R/2]: with R = 128 the
  * tables of svdq_w4a4_gemm_qkv_norm_rope.

@@ -127,6 +127,25 @@ def test_gemm(M, N, K, epilogue):
     _check_gemm(host(y), qx, sx, qw, sw, bias, epilogue)
 
 
+@pytest.mark.parametrize("M", [2, 300])
+def test_gelu_tails(M):
+    """Arguments that are exact (small integers over 16), -7.9 to 7.9: the relative error
+    is the function's own, (3.5 |t| + 7) 2^-24 with 2^t its exponential, and the
+    rounding to bf16; fl32 constants and three roundings make up |t|'s share, the
+    exponential, the reciprocal (an ulp each), a sum and a product the rest."""
+    import bit_diffusion_transformer_svdq_amd as P
+    qx, qw = np.zeros((M, 64), np.int8), np.zeros((256, 64), np.int8)
+    qx[:, 5] = 1
+    qw[:, 5] = np.arange(-128, 128)
+    sx, sw = np.full(M, 2.0 ** -4, np.float32), np.ones(256, np.float32)
+    y = host(P.w8a8_gemm(dev(qx), dev(sx), dev(qw), dev(sw), epilogue="gelu_tanh"))
+    x = np.arange(-128, 128) / 16.0
+    u = np.sqrt(2 / np.pi) * (x + 0.044715 * x ** 3)
+    want = x / (1 + np.exp(-2 * u))
+    t = np.abs(2 * u * np.log2(np.e))
+    assert (np.abs(y - want) <= (2.0 ** -8 / (1 + 2.0 ** -8) + 1.01 * (3.5 * t + 7) * U) * np.abs(want)).all()
+
+
 @pytest.mark.parametrize("M", [3, 300])
 def test_gemm_largest_sums(M):
     """Every product 2^14: the largest int32 sum, 2^30, stays exact."""

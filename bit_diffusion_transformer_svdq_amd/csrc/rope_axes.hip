@@ -78,11 +78,13 @@ __device__ __forceinline__ float2 angle_of(const void* positions, int pos_int, i
   c = __builtin_fma(c, t2, 1.0 / 24.0);
   c = __builtin_fma(c, t2, -0.5);
   c = __builtin_fma(c, t2, 1.0);
-  // the quarter within its turn (exact; NaN stays NaN in s and c)
-  const int k = (int)(quarter - 4.0 * __builtin_floor(quarter * 0.25));
+  // the quarter within its turn, 0 to 3 (exact; for a position that is not finite
+  // s and c are NaN whatever it is)
+  const double k = quarter - 4.0 * __builtin_floor(quarter * 0.25);
+  const bool odd = k == 1.0 || k == 3.0;
   const float fs = (float)s, fc = (float)c;
-  const float x = (k & 1) != 0 ? fs : fc, y = (k & 1) != 0 ? fc : fs;
-  return float2{k == 1 || k == 2 ? -x : x, (k & 2) != 0 ? -y : y};
+  const float x = odd ? fs : fc, y = odd ? fc : fs;
+  return float2{k == 1.0 || k == 2.0 ? -x : x, k >= 2.0 ? -y : y};
 }
 
 __global__ __launch_bounds__(kThreads) void rope_tables_kernel(const TableArgs a) {

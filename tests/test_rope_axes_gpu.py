@@ -49,6 +49,25 @@ def test_tables(axes, P, kind, spectrum):
     assert np.abs(host(c) - np.cos(t)).max() <= e and np.abs(host(s) - np.sin(t)).max() <= e
 
 
+def test_positions_that_are_not_finite():
+    """Their axis's channels become NaN; other axes and tokens are as without them."""
+    import torch
+    import bit_diffusion_transformer_svdq_amd as K
+    g = np.random.default_rng(8)
+    pos = _pos(g, 9, 2, "fraction")
+    bad = pos.copy()
+    bad[1, 0], bad[4, 1], bad[6, 0] = np.nan, np.inf, -np.inf
+    axes = (16, 24)
+    q = dev_bf16(bf16(g.standard_normal((9, 3, 48))))
+    for t, b in zip((*K.rope_axes_tables(dev(pos), axes), K.rope_axes(q, None, dev(pos), axes)[0]),
+                    (*K.rope_axes_tables(dev(bad), axes), K.rope_axes(q, None, dev(bad), axes)[0])):
+        w = 2 if t.dim() == 3 else 1
+        lost = torch.zeros_like(t, dtype=torch.bool)
+        for m, lo, hi in ((1, 0, 8), (6, 0, 8), (4, 8, 20)):
+            lost[m, ..., w * lo:w * hi] = True
+        assert bool(b[lost].isnan().all()) and torch.equal(b[~lost], t[~lost])
+
+
 def _check_turn(got, v, w, pos, axes, theta, spectrum, layout, eps=1e-6):
     n, en = (np.asarray(v), np.zeros_like(v)) if w is None else norm_bound(v, np.zeros_like(v), "rms", eps)
     if w is not None:

@@ -45,7 +45,7 @@ def _device(t, stream, name):
         if t.numel():
             raise ValueError(f"{name}: must be a device tensor")
         return idx
-    here = torch.cuda.current_device()
+    here = _here()
     if idx != here or (stream is not None and stream.device_index != here):
         raise ValueError(f"{name}: the tensors, the stream and the current device (cuda:{here}) must agree")
     return idx
@@ -56,8 +56,10 @@ def _current_stream(idx):
 
 
 # the handle of the current stream without a Stream object around it (2 us less
-# per call), where this torch has it
+# per call), and the current device without a look at the initialization (a device
+# tensor is in hand), where this torch has them
 _raw_current = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+_here = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _raw_stream(idx, stream):
@@ -74,6 +76,12 @@ def _new(like, dtype, stream, *shape):
     n = len(shape)
     strides = (1,) if n == 1 else (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1)
     return torch.empty_strided(shape, strides, dtype=dtype, device=like.device)
+
+
+def _new_like(t, stride, stream, *shape):
+    """_new of t's own type and shape; empty_like is the quicker where t's rows are dense."""
+    width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
+    return torch.empty_like(t) if stream is None and stride == width else _new(t, t.dtype, stream, *shape)
 
 
 def _hold(stream, *tensors):
@@ -129,6 +137,15 @@ def _rows(t, dtype, shape, idx, name):
         else:
             return t.data_ptr(), strides[0] if shape[0] > 1 else width
     _refuse(t, dtype, shape, idx, name)
+
+
+def _rows2(t, dtype, rows, width, idx, name):
+    """_rows of a matrix, the common case, in one look at its strides."""
+    if t.dtype is dtype and t.get_device() == idx and t.shape == (rows, width):
+        stride, step = t.stride()
+        if step == 1 or width == 1:
+            return t.data_ptr(), stride if rows > 1 else width
+    _refuse(t, dtype, (rows, width), idx, name)
 
 
 def quantize_act_int8(x, smooth=None, out=None, stream=None):
@@ -209,7 +226,7 @@ def gate_norm_modulate(x, y=None, post_norm="none", post_weight=None, gate=None,
     M, C = x.shape
     idx = _device(x, stream, "x")
     fp32 = x.dtype is torch.float32
-    px, xs = _rows(x, torch.float32 if fp32 else _BF16, (M, C), idx, "x")
+    px, xs = _rows2(x, torch.float32 if fp32 else _BF16, M, C, idx, "x")
     post, kind = _choice(_NORMS, post_norm, "post_norm"), _choice(_NORMS, norm, "norm")
     if quantize not in (None, "int8"):
         raise ValueError(f"quantize: expected None or 'int8', got {quantize!r}")
@@ -217,29 +234,29 @@ def gate_norm_modulate(x, y=None, post_norm="none", post_weight=None, gate=None,
     ys = hs = gr = gs = mr = ms = 0
     h = z = None
     if y is not None:
-        py, ys = _rows(y, _BF16, (M, C), idx, "y")
+        py, ys = _rows2(y, _BF16, M, C, idx, "y")
         if h_out is None:
-            h = _new(x, x.dtype, stream, M, C)
+            h = _new_like(x, xs, stream, M, C)
             ph, hs = h.data_ptr(), C
         else:
             h = h_out
-            ph, hs = _rows(h, x.dtype, (M, C), idx, "h")
+            ph, hs = _rows2(h, x.dtype, M, C, idx, "h")
     elif h_out is not None:
         raise ValueError("h_out: there is no h without y")
     if post_weight is not None:
         ppw = _dense(post_weight, _BF16, (C,), idx, "post_weight")
     if gate is not None:
         gr = gate.shape[0]
-        pg, gs = _rows(gate, _BF16, (gr, C), idx, "gate")
+        pg, gs = _rows2(gate, _BF16, gr, C, idx, "gate")
     if weight is not None:
         pw = _dense(weight, _BF16, (C,), idx, "weight")
     if scale is not None:
         mr = scale.shape[0]
-        psc, ms = _rows(scale, _BF16, (mr, C), idx, "scale")
+        psc, ms = _rows2(scale, _BF16, mr, C, idx, "scale")
     if shift is not None:
         if scale is None:
             mr = shift.shape[0]
-        psh, shs = _rows(shift, _BF16, (mr, C), idx, "shift")
+        psh, shs = _rows2(shift, _BF16, mr, C, idx, "shift")
         if scale is not None and shs != ms:
             raise ValueError("scale and shift: the row strides differ")
         ms = shs
@@ -247,8 +264,12 @@ def gate_norm_modulate(x, y=None, post_norm="none", post_weight=None, gate=None,
         psm = _dense(smooth, torch.float32, (C,), idx, "smooth")
     if kind:
         if quantize is None:
-            z = _new(x, _BF16, stream, M, C) if out is None else out
-            pz = z.data_ptr() if out is None else _dense(z, _BF16, (M, C), idx, "z")
+            if out is None:
+                z = _new(x, _BF16, stream, M, C) if fp32 else _new_like(x, xs, stream, M, C)
+                pz = z.data_ptr()
+            else:
+                z = out
+                pz = _dense(z, _BF16, (M, C), idx, "z")
         else:
             if out is None:
                 z = _new(x, torch.int8, stream, M, C), _new(x, torch.float32, stream, M)
@@ -324,10 +345,10 @@ def rope_axes(q, k, positions, axes, theta=10000.0, spectrum="axis", layout="pai
         Hk = k.shape[1]
         pk, ks = _rows(k, _BF16, (M, Hk, D), idx, "k")
     if out is None:
-        qo = _new(q, _BF16, stream, M, Hq, D)
+        qo = _new_like(q, qs, stream, M, Hq, D)
         pqo, qos, ko = qo.data_ptr(), Hq * D, None
         if k is not None:
-            ko = _new(q, _BF16, stream, M, Hk, D)
+            ko = _new_like(k, ks, stream, M, Hk, D)
             pko, kos = ko.data_ptr(), Hk * D
     else:
         qo, ko = out

@@ -18,9 +18,10 @@
 // squares: no cancellation), W waves per row and V vectors of 8 channels per lane.
 // One row per workgroup (with W = 1: per wave) measured fastest: runs of rows with
 // the shared vectors in registers and the next row in flight lost more to
-// occupancy than they saved (4608 x 3072: 23.6-26 us against 22.7).  Only with a
-// smoothing vector, whose reciprocals are the dearest part, a workgroup takes a
-// run of rows and keeps the reciprocals (quantizer 4608 x 3072: 16.2 -> 11.3 us).
+// occupancy than they saved (4608 x 3072, with the loads in an earlier order: 23.6 to
+// 26 us against 22.7).  Only with a smoothing vector, whose reciprocals are the
+// dearest part, a workgroup takes a run of rows and keeps the reciprocals (quantizer
+// 4608 x 3072: 16.2 -> 10.9 us).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -386,14 +387,15 @@ int waves_for(int64_t M, int c8, int per_lane) {
   return w;
 }
 // Measured on MI355X (us, W waves and V vectors; the best of each marked *):
-//  gate norm  4608 x 1536: W1V3 15.0, W2V2 14.7, W4V1 13.8*    4608 x 5120: W4V3 41.1*, W8V2 46.4
-//             4608 x 3072: W2V3 24.7, W4V2 24.5, W8V1 24.2*    4608 x 4096: W2V4 36.5, W4V2 31.4, W8V1 31.2*
-//             8346 x 2304 fp32: W2V3 49.8*, W4V2 50.8          2304 x 8192: W4V4 35.1, W8V2 33.3*
-//  quantizer  4608 x 3072: W1V6 8.6*, W4V2 9.1, W8V1 10.1;  smoothed: W2V3 11.3*, W4V2 12.1
-//             4608 x 12288: W4V6 29.2, W8V3 28.2*, W16V2 30.8;  smoothed: W8V3 35.2*, W16V2 38.0
+//  gate norm  4608 x 1536: W1V3 12.5*, W2V2 13.0, W4V1 13.1    4608 x 5120: W4V3 37.1*, W8V2 40.8
+//             4608 x 3072: W2V3 20.9*, W4V2 21.7, W8V1 24.6    4608 x 4096: W2V4 31.0, W4V2 29.4*, W8V1 31.5
+//             8346 x 2304 fp32: W2V3 43.9*, W4V2 47.8          2304 x 8192: W4V4 31.5, W8V2 29.7*
+//  quantizer  1333 x 1920: W1V4 3.5*, W2V2 3.7;  1000 x 16384: W4V8 9.8*, W16V2 10.4
+//             4608 x 3072: W1V6 8.6*, W2V3 8.6*, W4V2 9.2, W8V1 10.1;  smoothed: W1V6 16.0, W2V3 10.8*, W4V2 11.2
+//             4608 x 12288: W4V6 29.0, W8V3 28.9*, W16V2 32.0;  smoothed: W4V6 49.4, W8V3 34.5*, W16V2 36.6
 //             smoothed, 2048 x 6144: W4V3 10.8*, W8V2 11.5;  1024 x 4608: W4V3 7.0*, W8V2 7.9;
 //             512 x 3072: W2V3 4.8, W4V2 4.4*
-//  The norm with 8-bit output keeps reciprocals too: 4608 x 3072 W2V3 28.2, W4V2 25.6.
+//  The norm with 8-bit output and reciprocals: 4608 x 3072 W2V3 27.3, W4V2 24.1*, W8V1 29.5.
 constexpr int kNormPerLane = 3, kNormInt8PerLane = 2, kQuantPerLane = 8, kQuantSmoothPerLane = 3;
 
 // Rows per run: one, or with a smoothing vector as many as leave kWavesPerCu

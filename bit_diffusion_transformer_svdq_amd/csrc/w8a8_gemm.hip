@@ -566,8 +566,8 @@ void set_w8a8_plan_override(int tile, int splits) {
 
 // The weight-streaming kernel for up to 4 tokens, and up to 16 where its workgroups
 // (one per 16 channels) are fewer than two per compute unit.  Measured, it against the
-// best tile: 1 token 3072 -> 3072 5.5 / 7.3 us, 3072 -> 12288 9.6 / 9.8, 12288 -> 3072 10.5 / 14.7;
-// 16 tokens 6.3 / 7.4, 12.1 / 10.2, 14.4 / 15.1.
+// best tile: 1 token 3072 -> 3072 5.6 / 8.2 us, 3072 -> 12288 9.6 / 9.7, 12288 -> 3072 10.2 / 14.2;
+// 16 tokens 6.1 / 8.1, 11.8 / 10.0, 14.3 / 14.4.
 static bool few_tokens(int64_t M, int64_t N) {
   const int t = g_tile.load(std::memory_order_relaxed);
   return t == 1 ? M <= 16 : t == 0 && (M <= 4 || (M <= 16 && N / 16 < 2 * current_cus()));

@@ -36,17 +36,19 @@ bool meet(const Rows& a, const Rows& b) {
   return d < a.width || d + b.width > a.stride;
 }
 
-// `out` must not meet any of `others`, except that it may be `same`: the same
-// address, stride and width (each element is read before it is written)
-svdq_status check_rows(const Rows& out, std::initializer_list<Rows> others, const void* same = nullptr,
-                       size_t same_stride = 0) {
-  for (const Rows& o : others) {
-    if (same && o.p == same && out.p == same && out.stride == same_stride && o.stride == same_stride &&
-        o.width == out.width)
-      continue;
+svdq_status check_rows(const Rows& out, std::initializer_list<Rows> others) {
+  for (const Rows& o : others)
     if (meet(out, o)) return fail(SVDQ_STATUS_INVALID_VALUE, "output %s overlaps %s", out.name, o.name);
-  }
   return SVDQ_STATUS_SUCCESS;
+}
+
+// `in` as check_rows takes it, or nothing where its rows are exactly those of
+// `out`: an update in place, of an input that each thread reads at its own places
+// before it writes them
+Rows unless_in_place(const Rows& out, const Rows& in) {
+  const bool same = in.p == out.p && in.width == out.width && in.rows == out.rows &&
+                    (in.stride == out.stride || in.rows == 1);
+  return same ? Rows{} : in;
 }
 
 bool bad_ptr(const void* p) { return p && !aligned16(p); }
@@ -213,7 +215,13 @@ svdq_status svdq_gate_norm_modulate(const void* x, int stream_type, int64_t x_st
       rh{has_y ? h : nullptr, (size_t)h_stride * e, c * e, m, "h"},
       rz{has_z ? z : nullptr, c * (q8 ? 1 : 2), c * (q8 ? 1 : 2), m, "z"},
       rzs{q8 ? z_scales : nullptr, 0, m * 4, 1, "z_scales"};
-  svdq_status s = check_rows(rh, {rx, ry, rg, rsc, rsh, rpw, rw, rsm, rz, rzs}, x, rx.stride);
+  // h may be x, and with it y, or a gate of M rows, where these are x too: a row's x,
+  // y and gate are read before its h is written, scale and shift after it
+  svdq_status s = SVDQ_STATUS_SUCCESS;
+  if (has_y && unless_in_place(rh, rx).p == nullptr)
+    s = check_rows(rh, {unless_in_place(rh, ry), unless_in_place(rh, rg), rsc, rsh, rpw, rw, rsm, rz, rzs});
+  else
+    s = check_rows(rh, {rx, ry, rg, rsc, rsh, rpw, rw, rsm, rz, rzs});
   if (s == SVDQ_STATUS_SUCCESS) s = check_rows(rz, {rx, ry, rg, rsc, rsh, rpw, rw, rsm, rzs});
   if (s == SVDQ_STATUS_SUCCESS) s = check_rows(rzs, {rx, ry, rg, rsc, rsh, rpw, rw, rsm});
   if (s != SVDQ_STATUS_SUCCESS) return s;
@@ -320,11 +328,8 @@ svdq_status svdq_rope_axes(const void* q, int64_t q_stride, int64_t q_heads, con
       rp{positions, 0, (size_t)position_rows * (size_t)n_axes * 4, 1, "positions"}, rqn{q_norm, 0, d * 2, 1, "q_norm"},
       rkn{k_norm, 0, d * 2, 1, "k_norm"}, oq{q_out, (size_t)q_out_stride * 2, (size_t)wq * 2, m, "q_out"},
       ok_{has_k ? k_out : nullptr, (size_t)k_out_stride * 2, (size_t)wk * 2, m, "k_out"};
-  s = check_rows(oq, {rq, rk, rp, rqn, rkn, ok_}, q, rq.stride);
-  // in place: q_out may be q itself, but not k
-  if (s == SVDQ_STATUS_SUCCESS && has_k && meet(oq, rk)) s = fail(SVDQ_STATUS_INVALID_VALUE, "output q_out overlaps k");
-  if (s == SVDQ_STATUS_SUCCESS && has_k) s = check_rows(ok_, {rk, rp, rqn, rkn}, k, rk.stride);
-  if (s == SVDQ_STATUS_SUCCESS && has_k && meet(ok_, rq)) s = fail(SVDQ_STATUS_INVALID_VALUE, "output k_out overlaps q");
+  s = check_rows(oq, {unless_in_place(oq, rq), rk, rp, rqn, rkn, ok_});
+  if (s == SVDQ_STATUS_SUCCESS && has_k) s = check_rows(ok_, {rq, unless_in_place(ok_, rk), rp, rqn, rkn});
   if (s != SVDQ_STATUS_SUCCESS) return s;
   s = check_current_device();
   if (s != SVDQ_STATUS_SUCCESS) return s;

@@ -523,7 +523,8 @@ svdq_status svdq_debug_set_w8a8_plan(int tile, int splits);
  *                divide M: row m takes row m / (M / rows)
  *   weight       device, bf16 [C] or NULL
  *   h            device out, x's type [M, C], rows h_stride apart; may be x itself
- *                with x's stride (the stream updated in place)
+ *                with x's stride (the stream updated in place; y, or a gate of M rows,
+ *                may then be x as well, and nothing else)
  *   z            device out, bf16 [M, C] or int8 [M, C]; z_scales fp32 [M] for int8
  *   smooth       device, fp32 [C] or NULL (int8 output only)
  * Strides are in elements and multiples of 8 (the chunks of a modulation

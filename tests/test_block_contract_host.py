@@ -1,0 +1,43 @@
+"""What the block operators' contract says about memory and sizes, checked without a
+GPU: every refusal comes before any HIP call, on pointers that are never read."""
+import ctypes
+
+import pytest
+
+from bit_diffusion_transformer_svdq_amd._lib import INVALID_VALUE, NO_DEVICE, SUCCESS, lib
+from tests.test_block_abi_host import NORM, ROPE, P, _call, _gpu_visible
+
+# a bf16 stream of four rows, updated in place, with bf16 output
+PLACE = dict(h=P(1), otype=0, smooth=None, zs=None, z=P(10))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(gate=P(1), gr=2, gs=128),                      # row m reads gate row m / 2, which another row's update writes
+    dict(scale=P(1), mr=2, ms=128), dict(shift=P(1), mr=2, ms=128),
+    dict(scale=P(1), mr=4, ms=128), dict(shift=P(1), mr=4, ms=128),   # read after the row's h is written
+    dict(scale=P(1), shift=P(1), mr=4, ms=128),
+    dict(gate=P(1), gr=1, gs=0), dict(w=P(1)), dict(pw=P(1)), dict(z=P(1)),
+    dict(y=P(1), ys=256), dict(h=P(8), hs=128, z=P(1)), dict(h=P(8), z=P(8))])
+def test_an_update_in_place_shares_its_rows_with_nothing_else(kw):
+    """h may be x itself; what a row reads after its h is written, or another row reads,
+    lies elsewhere."""
+    assert _call("svdq_gate_norm_modulate", NORM, dict(PLACE, **kw)) == INVALID_VALUE
+
+
+@pytest.mark.skipif(_gpu_visible(), reason="checks the no-GPU path")
+@pytest.mark.parametrize("name,defaults,kw", [
+    ("svdq_gate_norm_modulate", NORM, PLACE),
+    ("svdq_gate_norm_modulate", NORM, dict(PLACE, y=P(1))),             # the stream is its own block output
+    ("svdq_gate_norm_modulate", NORM, dict(PLACE, gate=P(1), gr=4, gs=128)),   # and its own gate, row by row
+    ("svdq_gate_norm_modulate", NORM, dict(PLACE, x=P(1), gate=P(1, 256), gr=4, gs=384, xs=384, hs=384)),  # between x's rows
+    ("svdq_gate_norm_modulate", NORM, dict(PLACE, h=P(8), gate=P(1), gr=4, gs=128, scale=P(1), shift=P(1), mr=4, ms=128)),
+    ("svdq_rope_axes", ROPE, dict(qo=P(1), qos=3072, ko=P(2), kos=3072))])
+def test_places_that_are_allowed(name, defaults, kw):
+    assert _call(name, defaults, kw) == NO_DEVICE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(qo=P(1), qos=3072, k=P(1), ks=3072, kh=8), dict(q=P(2), qh=2, ko=P(2), kos=3072), dict(qo=P(1), qos=3072, ko=P(1, 1024), kos=3072),
+    dict(q=P(1), k=P(1), qh=2, kh=2, qo=P(1), qos=3072, ko=P(1), kos=3072)])
+def test_a_turn_in_place_shares_its_rows_with_nothing_else(kw):
+    assert _call("svdq_rope_axes", ROPE, kw) == INVALID_VALUE

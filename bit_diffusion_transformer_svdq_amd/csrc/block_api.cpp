@@ -178,8 +178,9 @@ svdq_status svdq_gate_norm_modulate(const void* x, int stream_type, int64_t x_st
   if (!std::isfinite(eps) || eps < 0.0f) return fail(SVDQ_STATUS_INVALID_VALUE, "eps must be finite and >= 0");
   if (!std::isfinite(residual_scale)) return fail(SVDQ_STATUS_INVALID_VALUE, "residual_scale must be finite");
   const bool has_y = y != nullptr, has_z = norm != SVDQ_NORM_NONE, mod = scale || shift;
+  // (rows of an empty batch may be null, so they tell nothing of its parts)
   if (M > 0 && !has_y && !has_z) return fail(SVDQ_STATUS_INVALID_VALUE, "neither a block output nor a norm");
-  if (!has_y && (gate || post_weight || (M > 0 && post_norm != SVDQ_NORM_NONE)))
+  if (M > 0 && !has_y && (gate || post_weight || post_norm != SVDQ_NORM_NONE))
     return fail(SVDQ_STATUS_INVALID_VALUE, "gate and post norm need a block output y");
   if (!has_z && (weight || mod || smooth || q8))
     return fail(SVDQ_STATUS_INVALID_VALUE, "weight, scale, shift, smooth and 8-bit output need a norm");

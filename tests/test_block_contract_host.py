@@ -41,3 +41,23 @@ def test_places_that_are_allowed(name, defaults, kw):
     dict(q=P(1), k=P(1), qh=2, kh=2, qo=P(1), qos=3072, ko=P(1), kos=3072)])
 def test_a_turn_in_place_shares_its_rows_with_nothing_else(kw):
     assert _call("svdq_rope_axes", ROPE, kw) == INVALID_VALUE
+
+
+@pytest.mark.parametrize("kw", [dict(y=None), dict(y=None, h=None), dict(y=None, gate=None), dict(y=None, pw=None),
+                                dict(x=None, y=None, h=None, z=None, zs=None)])
+def test_no_rows_with_every_part(kw):
+    """An empty batch has null rows, and its gate, weights and modulation as ever."""
+    assert _call("svdq_gate_norm_modulate", NORM, dict(M=0, **kw)) == SUCCESS
+
+
+@pytest.mark.parametrize("quantize", [None, "int8"])
+def test_no_rows_through_the_binding(quantize):
+    import torch
+    import bit_diffusion_transformer_svdq_amd as pkg
+    bf = torch.bfloat16
+    x, v, w = torch.empty(0, 128, dtype=bf), torch.ones(2, 128, dtype=bf), torch.ones(128, dtype=bf)
+    h, z = pkg.gate_norm_modulate(x, x, post_norm="rms", post_weight=w, gate=v, weight=w, scale=v, shift=v,
+                                  quantize=quantize)
+    assert h.shape == (0, 128) and (z if quantize is None else z[0]).shape == (0, 128)
+    with pytest.raises(pkg.SvdqError):
+        pkg.gate_norm_modulate(x, x, norm="none", scale=v)

@@ -288,8 +288,14 @@ def gate_norm_modulate(x, y=None, post_norm="none", post_weight=None, gate=None,
     return h, z
 
 
+_MAX_ANGLES = 128  # angles of a head: half the axes' channels
+
+
 def _axes_array(axes):
-    return (ctypes.c_int64 * len(axes))(*axes)
+    a = (ctypes.c_int64 * len(axes))(*axes)
+    if a[:] != list(axes):
+        raise ValueError(f"axes: widths do not fit 64 bits: {tuple(axes)}")
+    return a
 
 
 def _positions(t, idx, n_axes):
@@ -313,14 +319,17 @@ def rope_axes_tables(positions, axes, theta=10000.0, spectrum="axis", out=None, 
     of which each axis owns a section."""
     idx = _device(positions, stream, "positions")
     pp, code, M = _positions(positions, idx, len(axes))
-    half = sum(axes) // 2
+    ax = _axes_array(axes)
+    half = sum(ax) // 2
     if out is None:
+        if not 0 < half <= _MAX_ANGLES:
+            half = 0  # the library refuses these axes: they ask for no memory first
         cos, sin = (_new(positions, torch.float32, stream, M, half) for _ in range(2))
     else:
         cos, sin = out
         _dense(cos, torch.float32, (M, half), idx, "cos")
         _dense(sin, torch.float32, (M, half), idx, "sin")
-    check(lib().svdq_rope_axes_tables(pp, code, M, len(axes), _axes_array(axes), theta,
+    check(lib().svdq_rope_axes_tables(pp, code, M, len(axes), ax, theta,
                                       _choice(_SPECTRA, spectrum, "spectrum"), cos.data_ptr(), sin.data_ptr(),
                                       _raw_stream(idx, stream)), "svdq_rope_axes_tables")
     if stream is not None:

@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from bit_diffusion_transformer_svdq_amd._lib import INVALID_VALUE, NO_DEVICE, SUCCESS, lib
+from bit_diffusion_transformer_svdq_amd._lib import INVALID_VALUE, NO_DEVICE, NOT_SUPPORTED, SUCCESS, lib
 from tests.test_block_abi_host import NORM, ROPE, P, _call, _gpu_visible
 
 # a bf16 stream of four rows, updated in place, with bf16 output
@@ -61,3 +61,26 @@ def test_no_rows_through_the_binding(quantize):
     assert h.shape == (0, 128) and (z if quantize is None else z[0]).shape == (0, 128)
     with pytest.raises(pkg.SvdqError):
         pkg.gate_norm_modulate(x, x, norm="none", scale=v)
+
+
+@pytest.mark.parametrize("axes,status", [((-2,), INVALID_VALUE), ((), INVALID_VALUE), ((1 << 40,), NOT_SUPPORTED), ((1 << 62, 1 << 62), NOT_SUPPORTED),
+                                         ((-2, 66), INVALID_VALUE), ((3,), INVALID_VALUE), ((258,), NOT_SUPPORTED), ((0,), INVALID_VALUE)])
+def test_axes_are_refused_before_outputs_are_made(axes, status, monkeypatch):
+    """Widths that the library refuses never decide how much memory is asked for, and
+    widths past 64 bits do not wrap."""
+    import torch
+    import bit_diffusion_transformer_svdq_amd as pkg
+    from bit_diffusion_transformer_svdq_amd import block
+    asked = []
+    real = torch.empty_strided
+    monkeypatch.setattr(block.torch, "empty_strided", lambda shape, *a, **kw: (asked.append(shape), real(shape, *a, **kw))[1])
+    with pytest.raises(pkg.SvdqError) as e:
+        pkg.rope_axes_tables(torch.empty(0, len(axes)), axes)
+    assert e.value.status == status
+    assert all(len(s) == 2 and 0 <= s[1] <= 128 for s in asked)
+    wide = tuple(axes) + ((1 << 64) + 64, 64 - (1 << 64))
+    q = torch.empty(0, 2, 64, dtype=torch.bfloat16)
+    for call in (lambda: pkg.rope_axes_tables(torch.empty(0, len(wide)), wide),
+                 lambda: pkg.rope_axes(q, None, torch.empty(0, len(wide)), wide)):
+        with pytest.raises(ValueError, match="axes"):
+            call()

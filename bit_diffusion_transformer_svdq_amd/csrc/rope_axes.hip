@@ -11,11 +11,12 @@
 // "Quantisierung von Modellen mit strukturellen Umschreibungen"); the kernel
 // here turns the Q and K of any other projection.
 //
-// Angles: the rates arrive in quarter turns per unit of position, as doubles;
-// the product with the position, its reduction to [-1/2, 1/2] quarter turns and the
-// Taylor series of sine and cosine (to t^13 and t^14: below 2^-45 at pi/4) are done in
-// double, about 20 operations per angle, so that a far position keeps the 2^-24 of a
-// near one and each value is rounded once.
+// Angles: the rates arrive in quarter turns per unit of position, each as a double
+// and what that leaves.  The product with the position, unrounded, its reduction to
+// [-1/2, 1/2] quarter turns and the Taylor series of sine and cosine (to t^13 and t^14:
+// below 2^-45 at pi/4) are done in double, about 22 operations per angle.  Up to |position| = 2^31 (any int32) the angle is then within
+// 2^-28 for theta of 1e4 and more (one rate in 64 bits, below 2^-60 of it), and each value
+// is rounded to fp32 once; with the double alone it is off by up to 2^-21.6 there.
 //
 // The turn is bound by HBM: Q and K are read and written once.  A workgroup
 // computes the angles of its tokens once, in LDS, for all their heads, while the
@@ -37,9 +38,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;  // per workgroup; with 8192 heads 2^15 items
 
+// one 16-byte load per angle
+struct Rate {
+  double per_unit;  // quarter turns per unit of position
+  float rest;       // what the double leaves of the rate
+  int axis;
+};
 struct Rates {
-  double per_unit[kRopeMaxAngles];  // quarter turns per unit of position
-  uint8_t axis[kRopeMaxAngles];
+  Rate of[kRopeMaxAngles];
 };
 
 struct TurnArgs {
@@ -59,11 +65,20 @@ struct TableArgs {
   int M;
 };
 
-__device__ __forceinline__ float2 angle_of(const void* positions, int pos_int, int64_t at, double rate) {
+// the row of positions starts at `row`
+__device__ __forceinline__ float2 angle_of(const void* positions, int pos_int, int64_t row, const Rate& f) {
+  const int64_t at = row + f.axis;
+  const double rate = f.per_unit, rest = (double)f.rest;
   const double p = pos_int ? (double)static_cast<const int32_t*>(positions)[at]
                            : (double)static_cast<const float*>(positions)[at];
   const double turns = p * rate, quarter = __builtin_rint(turns);
-  const double t = (turns - quarter) * 1.5707963267948966, t2 = t * t;
+  // the product again, unrounded, less its quarters.  Past 2^45 quarters (fp32 positions
+  // 2^22 apart) what the rounding leaves would pass the series' range in the end: those
+  // turn by whole quarters (NaN where they are not finite)
+  double t = __builtin_fma(p, rest, __builtin_fma(p, rate, -quarter));
+  if (!(__builtin_fabs(turns) < 0x1p45)) t = quarter * 0.0;
+  t *= 1.5707963267948966;
+  const double t2 = t * t;
   double s = 1.0 / 6227020800.0, c = -1.0 / 87178291200.0;
   s = __builtin_fma(s, t2, -1.0 / 39916800.0);
   s = __builtin_fma(s, t2, 1.0 / 362880.0);
@@ -93,7 +108,7 @@ __global__ __launch_bounds__(kThreads) void rope_tables_kernel(const TableArgs a
   if (at >= n) return;
   const int64_t m = at / a.half;
   const int i = (int)(at - m * a.half);
-  const float2 cs = angle_of(a.positions, a.pos_int, m * a.n_axes + a.f.axis[i], a.f.per_unit[i]);
+  const float2 cs = angle_of(a.positions, a.pos_int, m * a.n_axes, a.f.of[i]);
   a.cos[at] = cs.x;
   a.sin[at] = cs.y;
 }
@@ -275,7 +290,7 @@ __global__ __launch_bounds__(kThreads) void rope_turn_kernel(const TurnArgs t) {
   for (int e = tid; e < nt * half; e += kThreads) {
     const int tok = e / half, i = e - tok * half;
     const int64_t p = (m0 + tok) % a.pos_rows;
-    ang[e] = angle_of(a.positions, a.pos_int, p * a.n_axes + t.f.axis[i], t.f.per_unit[i]);
+    ang[e] = angle_of(a.positions, a.pos_int, p * a.n_axes, t.f.of[i]);
   }
   __syncthreads();
   for (; it < items; it += 2 * step) {
@@ -288,7 +303,8 @@ __global__ __launch_bounds__(kThreads) void rope_turn_kernel(const TurnArgs t) {
 
 // rate of angle i in quarter turns: theta^(-2j/d) / (pi/2), j and d within the
 // axis, or theta^(-2i/R) / (pi/2).  A running product in extended precision
-// (error below 2^-56 over 128 steps).
+// (step j is off by about 1.5 j 2^-63 of the rate: below 2^-60 of the fastest one
+// for theta of 1e4 and more, where the rate falls as j grows).
 void make_rates(const RopeAxes& x, Rates& f) {
   const long double quarter = 1.5707963267948966192313216916398L;
   const long double lt = std::log((long double)x.theta);
@@ -300,8 +316,9 @@ void make_rates(const RopeAxes& x, Rates& f) {
     const long double step = pairs > 0 ? std::exp(-lt / (long double)pairs) : 1.0L;
     long double v = 1.0L / quarter;
     for (int j = 0; j < pairs; ++j, ++at) {
-      f.per_unit[at] = (double)(x.shared ? all : v);
-      f.axis[at] = (uint8_t)ax;
+      const long double rate = x.shared ? all : v;
+      const double top = (double)rate;
+      f.of[at] = Rate{top, (float)(rate - (long double)top), ax};
       v *= step;
       all *= all_step;
     }

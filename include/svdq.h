@@ -550,8 +550,11 @@ svdq_status svdq_gate_norm_modulate(
  *   angle_i = position[axis of i] * rate_i,   i = 0 .. R/2 - 1, axis by axis
  *   rate_i  = theta^(-2 j / axes[a])  for the j-th angle of axis a (SVDQ_SPECTRUM_AXIS)
  *           = theta^(-2 i / R)                                     (SVDQ_SPECTRUM_SHARED)
- * The product, its reduction and the sine and cosine are done in double, so far
- * positions keep their precision and each value is rounded to fp32 once.
+ * The rate is kept to 64 bits and the product, its reduction and the sine and
+ * cosine are done in double with the product's remainder: for |position| up to 2^31
+ * (any int32) and theta >= 1e4 the angle is within 2^-28, and each value is rounded to
+ * fp32 once.  An fp32 position farther out loses precision in proportion, past
+ * 2^45 quarter turns it turns by whole quarters; one that is not finite gives NaN.
  *
  * svdq_rope_axes_tables writes cos and sin, fp32 [M, R/2]: with R = 128 the
  * tables of svdq_w4a4_gemm_qkv_norm_rope.

@@ -33,3 +33,51 @@ def test_a_stream_that_is_its_own_block_output_or_gate(M, C, parts):
     h, z = P.gate_norm_modulate(x, y, gate=gate, h_out=x, **kw)
     assert h is x and torch.equal(x, h0) and torch.equal(z, z0)
     assert bool(np.isfinite(x.float().cpu().numpy()).all())
+
+
+def _angle_bound(pos, axes, theta, spectrum):
+    """Error of an angle, kernel and oracle together, in radians: both keep a rate to 64 bits
+    (the kernel's, step j of a running product, to 1.5 j + 2 ln(1/rate) + 2 of them, the oracle's
+    exponential to ln(1/rate) + 4), products and reductions below 2^-44."""
+    n = [d // 2 for d in axes]
+    j = np.concatenate([np.arange(k) for k in n]) if spectrum == "axis" else np.arange(sum(n))
+    per = np.repeat(n, n) if spectrum == "axis" else np.full(sum(n), sum(n))
+    fall = j / per * np.log(theta)   # ln(1 / rate)
+    own = np.repeat(np.arange(len(axes)), n)
+    return 2.0 ** -44 + np.abs(pos[:, own].astype(np.float64)) * np.exp(-fall) * (1.5 * j + 3 * fall + 6) * 2.0 ** -63
+
+
+@pytest.mark.parametrize("axes", [(128,), (16, 56, 56), (2,), (64, 64, 64, 64)])
+@pytest.mark.parametrize("spectrum", ["axis", "shared"])
+@pytest.mark.parametrize("theta", [1e4, 1e6])
+@pytest.mark.parametrize("kind", ["int", "float"])
+def test_far_positions_keep_the_precision_of_near_ones(axes, spectrum, theta, kind):
+    """Up to 2^31 the tables are rounded once: half a step below one, 2^-25, beyond the
+    angle's own error."""
+    import oracle.block_oracle as B
+    import bit_diffusion_transformer_svdq_amd as P
+    from tests.block_util import dev, host
+    g = np.random.default_rng([3, len(axes)])
+    pos = g.integers(-2 ** 31, 2 ** 31 - 1, (600, len(axes)))
+    pos[0], pos[1] = -2 ** 31, 2 ** 31 - 1
+    pos = pos.astype(np.int32 if kind == "int" else np.float32)
+    t = B.rope_angles(pos, axes, theta, spectrum)
+    e = 2.0 ** -25 + _angle_bound(pos, axes, theta, spectrum)
+    c, s = P.rope_axes_tables(dev(pos), axes, theta=theta, spectrum=spectrum)
+    assert (np.abs(host(c) - np.cos(t)) <= e).all() and (np.abs(host(s) - np.sin(t)) <= e).all()
+
+
+def test_positions_too_far_for_an_angle_still_turn():
+    """fp32 positions up to the largest: whatever the angle, a cosine and a sine of one."""
+    import torch
+    import bit_diffusion_transformer_svdq_amd as P
+    from tests.block_util import dev, host
+    pos = np.array([[s * 2.0 ** k] for k in range(32, 128) for s in (1.0, -1.9999999)], np.float32)
+    assert np.isfinite(pos).all()
+    c, s = (host(t) for t in P.rope_axes_tables(dev(pos), (64,)))
+    # two values rounded to fp32 on the circle: |c dc| + |s ds| <= 2^-25 (|c| + |s|), twice
+    assert (np.abs(c * c + s * s - 1) <= 2 * 2.0 ** -25 * np.sqrt(2) + 2.0 ** -40).all()
+    q = torch.randn(len(pos), 2, 64, device="cuda").bfloat16()
+    qo, _ = P.rope_axes(q, None, dev(pos), (64,))
+    n0, n1 = (t.float().view(-1, 2, 32, 2).square().sum(-1) for t in (q, qo))
+    assert bool(((n0 - n1).abs() <= 2.0 ** -6 * n0).all())

@@ -470,7 +470,8 @@ svdq_status svdq_awq_w4a16_gemm_stacked(
  * svdq_w8a8_gemm:
  *   Y[m,n] = bf16( epi( (sum_k q_x[m,k] q_w[n,k]) * fl32(s_x[m] s_w[n]) + bias[n] ) )
  *   the sum exact in int32 (any codes, -128 included), one fp32 fma, epi none or
- *   GELU (svdq_epilogue), one bf16 rounding.
+ *   GELU (svdq_epilogue; results below 1.2e-37 in magnitude, x < -10, may be -0), one
+ *   bf16 rounding.
  *   act_codes int8 [M, K], act_scales fp32 [M], w_codes int8 [N, K], w_scales
  *   fp32 [N] (svdq_pack_weights_int8), bias bf16 [N] or NULL, y bf16 [M, N]
  *   workspace of svdq_w8a8_gemm_workspace_size(M, N, K) bytes (see Conventions):

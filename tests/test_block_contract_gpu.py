@@ -81,3 +81,28 @@ def test_positions_too_far_for_an_angle_still_turn():
     qo, _ = P.rope_axes(q, None, dev(pos), (64,))
     n0, n1 = (t.float().view(-1, 2, 32, 2).square().sum(-1) for t in (q, qo))
     assert bool(((n0 - n1).abs() <= 2.0 ** -6 * n0).all())
+
+
+@pytest.mark.parametrize("M", [2, 300])
+def test_gelu_to_the_end_of_its_tail(M):
+    """Exact arguments from -12 to -8.  While 2^t = exp(-2u) stays below 2^126 the relative
+    error is the function's own, (3.5 t + 7) 2^-24, and the rounding to bf16; beyond, where the
+    value is below 10.1 2^-126, it may come out as zero."""
+    import bit_diffusion_transformer_svdq_amd as P
+    from tests.block_util import U, dev, dev_bf16, host
+    qx, qw = np.zeros((M, 64), np.int8), np.zeros((256, 64), np.int8)
+    qx[:, 5] = 1
+    qw[:, 5] = np.arange(-128, 128)
+    b = np.full(256, -10.0)
+    y = host(P.w8a8_gemm(dev(qx), dev(np.full(M, 2.0 ** -6, np.float32)), dev(qw), dev(np.ones(256, np.float32)), dev_bf16(b),
+                         epilogue="gelu_tanh"))
+    x = b + np.arange(-128, 128) / 64.0
+    u = np.sqrt(2 / np.pi) * (x + 0.044715 * x ** 3)
+    t = -2 * u * np.log2(np.e)
+    want = x / (1 + np.exp(-2 * u))
+    near = t < 125.9
+    rel = 2.0 ** -8 / (1 + 2.0 ** -8) + 1.01 * (3.5 * t + 7) * U
+    assert near.sum() > 100 and (~near).sum() > 100
+    assert (np.abs(y - want) <= rel * np.abs(want))[:, near].all()
+    assert (np.abs(want[~near]) <= 10.1 * 2.0 ** -125.9).all()
+    assert ((y[:, ~near] <= 0) & (y[:, ~near] >= (1 + rel[~near]) * want[~near])).all()

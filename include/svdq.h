@@ -563,7 +563,8 @@ svdq_status svdq_gate_norm_modulate(
  * svdq_rope_axes turns Q and K, token by token, all heads by the same angles:
  *   v = q head, or with q_norm  q / sqrt(mean(q^2) + eps) * q_norm   (per head)
  *   SVDQ_ROPE_PAIRS:  (v[2i], v[2i+1]) -> (v[2i] c - v[2i+1] s, v[2i] s + v[2i+1] c)
- *   SVDQ_ROPE_HALVES: the same of (v[i], v[i + R/2])
+ *   SVDQ_ROPE_HALVES: the same of (v[i], v[i + R/2]), the halves of all R channels (not
+ *                     of each axis's own)
  *   channels R .. head_dim - 1 are not turned (but normed)
  * in fp32, rounded to bf16 once.
  *

@@ -106,3 +106,28 @@ def test_gelu_to_the_end_of_its_tail(M):
     assert (np.abs(y - want) <= rel * np.abs(want))[:, near].all()
     assert (np.abs(want[~near]) <= 10.1 * 2.0 ** -125.9).all()
     assert ((y[:, ~near] <= 0) & (y[:, ~near] >= (1 + rel[~near]) * want[~near])).all()
+
+
+def test_outputs_given_with_another_stream_outlive_their_owner():
+    """An output given with a stream and freed at once is not handed out again while
+    that stream still has it to write; the stream is busy throughout."""
+    import torch
+    import bit_diffusion_transformer_svdq_amd as P
+    x = torch.randn(64, 4096, device="cuda").bfloat16()
+    want = P.quantize_act_int8(x)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = (torch.empty(64, 4096, dtype=torch.int8, device="cuda"), torch.empty(64, device="cuda"))
+    at = out[0].data_ptr()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    P.quantize_act_int8(x, out=out, stream=s)
+    del out
+    more = [torch.empty(64, 4096, dtype=torch.int8, device="cuda") for _ in range(4)]
+    assert not s.query(), "the stream ended before the memory was asked for"
+    assert all(t.data_ptr() != at for t in more)
+    for t in more:
+        t.fill_(7)
+    torch.cuda.synchronize()
+    assert all(bool((t == 7).all()) for t in more)
+    assert torch.equal(P.quantize_act_int8(x)[0], want[0])

@@ -15,7 +15,10 @@
 //
 // Bound by HBM: every element of x and y is read once and of h and z written
 // once.  A row stays in registers between its reductions (mean, then centered
-// squares: no cancellation), W waves per row and V vectors of 8 channels per lane.
+// squares: no cancellation), W waves per row and V vectors of 8 channels per lane;
+// only rows of more than 16384 channels (16 waves of 3 or 4 vectors: 32 to 197 registers
+// per lane go to scratch memory) do not fit: bf16 with both norms 1024 x 16384 31 us, 4.3
+// TB/s, 1024 x 24576 79 us, 2.6 TB/s, 1024 x 32768 202 us, 1.3 TB/s.
 // One row per workgroup (with W = 1: per wave) measured fastest: runs of rows with
 // the shared vectors in registers and the next row in flight lost more to
 // occupancy than they saved (4608 x 3072, with the loads in an earlier order: 23.6 to
@@ -400,7 +403,8 @@ constexpr int kNormPerLane = 3, kNormInt8PerLane = 2, kQuantPerLane = 8, kQuantS
 
 // Rows per run: one, or with a smoothing vector as many as leave kWavesPerCu
 // waves per compute unit; more where the launch would come near 2^32 threads, its
-// limit (2^24 rows of 4 waves).
+// limit (2^24 rows of 4 waves).  Up to that many rows a run is one row, whose
+// reciprocals then serve it alone (quantizer 1333 x 1920: 3.2 us, smoothed 4.8).
 constexpr int kWavesPerCu = 32;
 int run_for(int64_t M, int w, bool smooth) {
   const int64_t owners = std::min<int64_t>(smooth ? (int64_t)current_cus() * kWavesPerCu / w : M, (1 << 25) / w);

@@ -20,9 +20,8 @@
 //
 // The turn is bound by HBM: Q and K are read and written once.  A workgroup
 // computes the angles of its tokens once, in LDS, for all their heads, while the
-// first of them are being loaded.  4608 tokens of 24 + 24 heads of 128: 22.8 us normed,
-// 21.1 without, 5.0 and 5.4 TB/s; 32760 tokens of 12 + 12: 73.7 us, 5.5 TB/s (a copy of 1 GiB
-// runs at 5.1 TB/s).
+// first of them are being loaded.  4608 tokens of 24 + 24 heads of 128: 22 us normed,
+// 5.1 TB/s; 32760 tokens of 12 + 12: 72 us, 5.6 TB/s (a copy of 1 GiB runs at 5.2 TB/s).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -159,7 +158,8 @@ __device__ __forceinline__ float rsqrt_of(float x) {
 }
 
 // VEC channels per lane; a head takes `lanes` = the power of two >= D / VEC
-// lanes, those past D / VEC idle.  The (token, head) items of the workgroup are
+// lanes, those past D / VEC idle (4608 tokens of 48 normed heads: D = 64 4.7 TB/s, 80
+// 3.8, 96 4.5, 128 5.1, 256 4.4).  The (token, head) items of the workgroup are
 // dealt to its lane groups in order, kPer items of a group in flight together.
 template <int VEC, bool kHalves, bool kNorm>
 __global__ __launch_bounds__(kThreads) void rope_turn_kernel(const TurnArgs t) {

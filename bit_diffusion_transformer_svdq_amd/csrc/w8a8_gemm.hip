@@ -7,9 +7,9 @@
 //
 // With no dequantization inside the K loop the kernel is a plain int8 GEMM.  Large
 // products are bound by the chip's power: on random codes registers alone feed
-// v_mfma_i32_32x32x32_i8 at 3.45 POP/s and v_mfma_i32_16x16x64_i8, which touches its
-// accumulators half as often, at 4.15 (4.9 on zeros), so the second is used, and
-// operands are moved as little as the registers allow.
+// v_mfma_i32_32x32x32_i8 at 3.5 POP/s and v_mfma_i32_16x16x64_i8, which touches its
+// accumulators half as often, at 4.05 (both 4.9 on zeros; tests/probes/int8_rate_probe.hip),
+// so the second is used, and operands are moved as little as the registers allow.
 //  * workgroup tile 32 WI WN weight rows x 32 WJ WM token rows, WN x WM waves of
 //    2 WI x 2 WJ tiles of 16 x 16 (256 x 256 on 8 waves: 128 int32 accumulators per
 //    lane, two waves per SIMD);
@@ -25,7 +25,9 @@
 //    the same in the upper half) over 256 bytes of banks: in each phase the even
 //    and the odd rows then take 8 different slots, no two lanes one bank;
 //  * few tiles: K is split over workgroups, whose int32 partials meet in the
-//    caller's workspace (integer sums: the order does not matter);
+//    caller's workspace (integer sums: the order does not matter).  (The model below does
+//    not know of a caller who clears the workspace for each call, as in a captured graph:
+//    64 x 12288 -> 3072 12.0 us, captured 13.9);
 //  * many tiles: a workgroup stays and takes one after the other; the last R
 //    stages of a tile fetch the first of the next, and while its Y leaves they
 //    arrive (4608 x 3072 -> 12288 with GELU 165 -> 159 us, 16384 x 4096 -> 4096 221 -> 217).

@@ -193,6 +193,7 @@ svdq_status svdq_gate_norm_modulate(const void* x, int stream_type, int64_t x_st
   if ((gate && (gate_rows <= 0 || M % gate_rows != 0)) || (mod && (mod_rows <= 0 || M % mod_rows != 0)))
     return fail(SVDQ_STATUS_INVALID_VALUE, "gate rows %lld and modulation rows %lld must divide M=%lld",
                 (long long)gate_rows, (long long)mod_rows, (long long)M);
+  if (M == 1) x_stride = y_stride = h_stride = C;  // strides of one row are not read
   if (x_stride < C || (has_y && (y_stride < C || h_stride < C)) || (gate && gate_rows > 1 && gate_stride < C) ||
       (mod && mod_rows > 1 && mod_stride < C))
     return fail(SVDQ_STATUS_INVALID_VALUE, "a row stride is smaller than C=%lld", (long long)C);

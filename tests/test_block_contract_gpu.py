@@ -131,3 +131,20 @@ def test_outputs_given_with_another_stream_outlive_their_owner():
     torch.cuda.synchronize()
     assert all(bool((t == 7).all()) for t in more)
     assert torch.equal(P.quantize_act_int8(x)[0], want[0])
+
+
+def test_one_row_through_the_library_with_strides_of_nothing():
+    """M = 1: the strides of x, y and h are not read."""
+    import ctypes
+    import torch
+    import bit_diffusion_transformer_svdq_amd as P
+    from bit_diffusion_transformer_svdq_amd._lib import SUCCESS, lib
+    C = 320
+    x, y, h = (torch.randn(1, C, device="cuda").bfloat16() for _ in range(3))
+    z = torch.empty(1, C, device="cuda", dtype=torch.bfloat16)
+    want = P.gate_norm_modulate(x, y, norm="rms")
+    p = [ctypes.c_void_p(t.data_ptr()) for t in (x, y, h, z)]
+    st = lib().svdq_gate_norm_modulate(p[0], 0, 0, p[1], -8, 0, None, None, 0, 0, 1.0, 2, None, None, None, 0, 0, 1e-6, 1, C,
+                                       p[2], 3, 0, None, p[3], None, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert st == SUCCESS
+    assert torch.equal(h, want[0]) and torch.equal(z, want[1])

@@ -84,3 +84,15 @@ def test_axes_are_refused_before_outputs_are_made(axes, status, monkeypatch):
                  lambda: pkg.rope_axes(q, None, torch.empty(0, len(wide)), wide)):
         with pytest.raises(ValueError, match="axes"):
             call()
+
+
+@pytest.mark.skipif(_gpu_visible(), reason="checks the no-GPU path")
+@pytest.mark.parametrize("kw", [dict(xs=0, ys=0, hs=0), dict(xs=-8, ys=3, hs=1 << 60), dict(h=P(1), hs=0, xs=128), dict(h=P(1), hs=64, xs=7)])
+def test_strides_of_one_row_are_not_read(kw):
+    assert _call("svdq_gate_norm_modulate", NORM, dict(M=1, gr=1, gs=0, mr=1, ms=-5, **kw)) == NO_DEVICE
+
+
+def test_one_row_over_another_is_still_refused():
+    one = dict(M=1, gr=1, gs=0, mr=1, ms=0, xs=0, ys=0, hs=0)
+    for kw in (dict(h=P(1, 16)), dict(h=P(2)), dict(h=P(6)), dict(z=P(1, 128)), dict(h=P(1), scale=P(1))):
+        assert _call("svdq_gate_norm_modulate", NORM, dict(one, **kw)) == INVALID_VALUE

@@ -568,8 +568,10 @@ void set_w8a8_plan_override(int tile, int splits) {
 
 // The weight-streaming kernel for up to 4 tokens, and up to 16 where its workgroups
 // (one per 16 channels) are fewer than two per compute unit.  Measured, it against the
-// best tile: 1 token 3072 -> 3072 5.6 / 8.2 us, 3072 -> 12288 9.6 / 9.7, 12288 -> 3072 10.2 / 14.2;
-// 16 tokens 6.1 / 8.1, 11.8 / 10.0, 14.3 / 14.4.
+// best tile, in a graph, the weights from HBM: 1 token 3072 -> 3072 4.9 / 7.9 us, 3072 -> 12288
+// 9.3 / 10.7, 12288 -> 3072 11.0 / 13.0; 4 tokens 5.1 / 8.0, 10.1 / 10.8, 11.6 / 13.1; 16 tokens
+// 6.3 / 8.1, 13.8 / 11.0, 16.8 / 13.3 (the rule does not look at K: with a long one the
+// tiles are the quicker from 9 tokens or so, where they need no cleared workspace).
 static bool few_tokens(int64_t M, int64_t N) {
   const int t = g_tile.load(std::memory_order_relaxed);
   return t == 1 ? M <= 16 : t == 0 && (M <= 4 || (M <= 16 && N / 16 < 2 * current_cus()));

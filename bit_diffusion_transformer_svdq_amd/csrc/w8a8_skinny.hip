@@ -9,7 +9,7 @@
 // Two steps of 64 k are loaded together and the next two while they are computed:
 // deeper rings measured slower (1 token, 3072 -> 12288: 9.6 us with 2 steps, 11.1 with
 // 4), as did 16 and 4 waves.  9.6 us is 3.9 TB/s over the weights, launch included;
-// 3072 -> 3072 takes 5.6 us, 12288 -> 3072 10.2 us.  More rows per workgroup only pay where
+// 3072 -> 3072 takes 4.9 us, 12288 -> 3072 11 to 12 us.  More rows per workgroup only pay where
 // the tile kernel is faster still.
 
 #include <hip/hip_runtime.h>

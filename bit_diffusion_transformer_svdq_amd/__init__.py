@@ -24,7 +24,8 @@ paragraph on the 16-bit branch, names the two fusions):
 and the offline host packer (``smooth_from_absmax``, ``pack_weights``).
 
 The operators around these linears in a transformer block (the 8-bit linear,
-the gated residual norms, rotary positions with several axes) are in block.py.
+the gated residual norms, rotary positions with several axes) are in block.py, the
+8-bit floating-point linear and the gated feed-forward block on it in fp8.py.
 """
 from __future__ import annotations
 
@@ -42,14 +43,17 @@ __all__ = ["SvdqError", "lib", "check_device", "quantize_act_lora_down", "w4a4_g
            "quantize_act_lora_down_fp4", "fp4_gemm_lora_up", "pack_weights_fp4",
            "release_workspaces", "GROUP_SIZE",
            "quantize_act_int8", "w8a8_gemm", "pack_weights_int8", "gate_norm_modulate", "rope_axes",
-           "rope_axes_tables", "debug_set_w8a8_plan"]
+           "rope_axes_tables", "debug_set_w8a8_plan",
+           "quantize_act_fp8", "fp8_gemm", "fp8_gated_gemm", "gated_ffn_fp8", "pack_weights_fp8",
+           "debug_set_fp8_plan"]
 
 GROUP_SIZE = 64
 
-# the block operators live in block.py, which needs torch; it is imported when
-# one of them is first used
+# the block operators live in block.py and fp8.py, which need torch; each module is
+# imported when one of its operators is first used
 _BLOCK = ("quantize_act_int8", "w8a8_gemm", "pack_weights_int8", "gate_norm_modulate", "rope_axes",
           "rope_axes_tables", "debug_set_w8a8_plan")
+_FP8 = ("quantize_act_fp8", "fp8_gemm", "fp8_gated_gemm", "gated_ffn_fp8", "pack_weights_fp8", "debug_set_fp8_plan")
 
 
 def __getattr__(name):
@@ -57,6 +61,11 @@ def __getattr__(name):
         from . import block
         for n in _BLOCK:
             globals()[n] = getattr(block, n)
+        return globals()[name]
+    if name in _FP8:
+        from . import fp8
+        for n in _FP8:
+            globals()[n] = getattr(fp8, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

@@ -68,6 +68,18 @@ SIGNATURES = {
         _c_void_p, _c_void_p, _size, _c_void_p]),
     "svdq_w8a8_gemm_workspace_size": (_size, [_i64, _i64, _i64]),
     "svdq_debug_set_w8a8_plan": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
+    "svdq_quantize_act_fp8": (ctypes.c_int, [
+        _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i64, _c_void_p]),
+    "svdq_fp8_gemm": (ctypes.c_int, [
+        _c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, ctypes.c_int,
+        _c_void_p, _c_void_p, _size, _c_void_p]),
+    "svdq_fp8_gemm_workspace_size": (_size, [_i64, _i64, _i64]),
+    "svdq_fp8_gated_gemm": (ctypes.c_int, [
+        _c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+        _i64, _i64, _i64, ctypes.c_int, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _i64,
+        _c_void_p, _size, _c_void_p]),
+    "svdq_fp8_gated_gemm_workspace_size": (_size, [_i64, _i64, _i64, ctypes.c_int]),
+    "svdq_debug_set_fp8_plan": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
     "svdq_gate_norm_modulate": (ctypes.c_int, [
         _c_void_p, ctypes.c_int, _i64, _c_void_p, _i64, ctypes.c_int, _c_void_p, _c_void_p, _i64, _i64,
         ctypes.c_float, ctypes.c_int, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, ctypes.c_float, _i64, _i64,
@@ -80,6 +92,8 @@ SIGNATURES = {
         _c_void_p, ctypes.c_double, ctypes.c_int, ctypes.c_int, _c_void_p, _c_void_p, ctypes.c_float,
         _c_void_p, _i64, _c_void_p, _i64, _c_void_p]),
     "svdq_pack_weights_int8": (ctypes.c_int, [
+        _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p]),
+    "svdq_pack_weights_fp8": (ctypes.c_int, [
         _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p]),
     "svdq_w4a4_group_acc_debug": (ctypes.c_int, [
         _c_void_p, _c_void_p, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p]),

@@ -26,7 +26,9 @@ _NORMS = {"none": 0, "layer": 1, "rms": 2}
 _EPILOGUES = {"none": 0, "gelu_tanh": 1}
 _SPECTRA = {"axis": 0, "shared": 1}
 _LAYOUTS = {"pairs": 0, "halves": 1}
+_NORM_OUTS = {None: 0, "int8": 1, "fp8": 3}
 _BF16 = torch.bfloat16
+_E4M3 = torch.float8_e4m3fn
 _WS_COUNTERS = 1 << 20  # bytes of a workspace's arrival counters
 
 
@@ -218,18 +220,21 @@ def gate_norm_modulate(x, y=None, post_norm="none", post_weight=None, gate=None,
     M (row m takes row m // (M // B)) or None; weights bf16 [C] or None.  Rows of
     x, y, gate, scale, shift and h may be strided (chunks of a projection's output).
     ``quantize="int8"`` gives z as the codes and token scales of w8a8_gemm,
-    divided by ``smooth`` (fp32 [C]) first.
+    ``quantize="fp8"`` as the codes and block scales of fp8_gemm, divided by
+    ``smooth`` (fp32 [C]) first.
 
     Returns (h, z): h of x's type, None without y (``h_out`` may be x); z bf16
-    [M, C], or (int8 [M, C], fp32 [M]), or None for norm="none".
+    [M, C], or (int8 [M, C], fp32 [M]), or (float8_e4m3fn [M, C], fp32
+    [ceil(C / 128), M]), or None for norm="none".
     """
     M, C = x.shape
     idx = _device(x, stream, "x")
     fp32 = x.dtype is torch.float32
     px, xs = _rows2(x, torch.float32 if fp32 else _BF16, M, C, idx, "x")
     post, kind = _choice(_NORMS, post_norm, "post_norm"), _choice(_NORMS, norm, "norm")
-    if quantize not in (None, "int8"):
-        raise ValueError(f"quantize: expected None or 'int8', got {quantize!r}")
+    if quantize not in (None, "int8", "fp8"):
+        raise ValueError(f"quantize: expected None, 'int8' or 'fp8', got {quantize!r}")
+    out_type = _NORM_OUTS[quantize]
     py = ph = ppw = pg = pw = psc = psh = psm = pz = pzs = None
     ys = hs = gr = gs = mr = ms = 0
     h = z = None
@@ -271,18 +276,19 @@ def gate_norm_modulate(x, y=None, post_norm="none", post_weight=None, gate=None,
                 z = out
                 pz = _dense(z, _BF16, (M, C), idx, "z")
         else:
+            codes, shape = (torch.int8, (M,)) if quantize == "int8" else (_E4M3, (-(-C // 128), M))
             if out is None:
-                z = _new(x, torch.int8, stream, M, C), _new(x, torch.float32, stream, M)
+                z = _new(x, codes, stream, M, C), _new(x, torch.float32, stream, *shape)
                 pz, pzs = z[0].data_ptr(), z[1].data_ptr()
             else:
                 z = (out[0], out[1])
-                pz = _dense(z[0], torch.int8, (M, C), idx, "z codes")
-                pzs = _dense(z[1], torch.float32, (M,), idx, "z scales")
+                pz = _dense(z[0], codes, (M, C), idx, "z codes")
+                pzs = _dense(z[1], torch.float32, shape, idx, "z scales")
     elif out is not None:
         raise ValueError("out: there is no z with norm='none'")
     check(lib().svdq_gate_norm_modulate(
         px, int(fp32), xs, py, ys, post, ppw, pg, gr, gs, residual_scale, kind, pw, psc, psh, mr, ms, eps, M, C,
-        ph, hs, int(quantize is not None), psm, pz, pzs, _raw_stream(idx, stream)), "svdq_gate_norm_modulate")
+        ph, hs, out_type, psm, pz, pzs, _raw_stream(idx, stream)), "svdq_gate_norm_modulate")
     if stream is not None:
         _hold(stream, x, y, post_weight, gate, weight, scale, shift, smooth, h, *(z if isinstance(z, tuple) else (z,)))
     return h, z

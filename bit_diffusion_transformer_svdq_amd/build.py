@@ -34,8 +34,9 @@ ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HOST_API_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-D__HIP_PLATFORM_AMD__",
                   "-I", os.path.join(ROCM, "include")]
 KERNELS = ["quant_lora_down.hip", "w4a4_gemm_lora_up.hip", "w4a4_gemm_skinny.hip", "fp4_gemm_big.hip",
-           "awq_w4a16_gemm.hip", "w8a8_gemm.hip", "w8a8_skinny.hip", "gate_norm.hip", "rope_axes.hip"]
-HOST_API = ["api.cpp", "block_api.cpp"]
+           "awq_w4a16_gemm.hip", "w8a8_gemm.hip", "w8a8_skinny.hip", "gate_norm.hip", "rope_axes.hip",
+           "quant_fp8.hip", "fp8_gemm.hip", "fp8_skinny.hip"]
+HOST_API = ["api.cpp", "block_api.cpp", "fp8_api.cpp"]
 
 
 def _hipcc() -> str:

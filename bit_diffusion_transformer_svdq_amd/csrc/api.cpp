@@ -490,7 +490,7 @@ svdq_status svdq_w4a4_group_acc_debug(const void* act_codes, const void* w_codes
 
 }  // extern "C"
 
-// entry points in other files (packer.cpp, block_api.cpp) and the checks of
+// entry points in other files (packer.cpp, block_api.cpp, fp8_api.cpp) and the checks of
 // api_checks.h set the thread's message through these
 svdq_status svdq_internal_fail(svdq_status s, const char* msg) {
   snprintf(g_err, sizeof(g_err), "%s", msg);

@@ -1,4 +1,4 @@
-// Argument checks shared by the C ABI's entry points (api.cpp, block_api.cpp).
+// Argument checks shared by the C ABI's entry points (api.cpp, block_api.cpp, fp8_api.cpp).
 // Host only.
 #pragma once
 
@@ -78,6 +78,42 @@ inline svdq_status check_workspace(const void* ws, size_t ws_bytes, size_t need,
   if (!aligned16(ws)) return fail(SVDQ_STATUS_INVALID_VALUE, "workspace must be 16-byte aligned");
   return SVDQ_STATUS_SUCCESS;
 }
+
+// rows of `width` bytes, `stride` bytes apart
+struct Rows {
+  const void* p;
+  size_t stride, width, rows;
+  const char* name;
+};
+
+inline size_t extent(const Rows& r) { return r.rows == 0 ? 0 : (r.rows - 1) * r.stride + r.width; }
+
+// Whether two sets of rows may share a byte.  Rows of one stride can interleave
+// (the Q and K columns of one projection's output): their places within a
+// stride decide.
+inline bool meet(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p) return false;
+  if (!overlap({a.p, extent(a), a.name}, {b.p, extent(b), b.name})) return false;
+  if (a.stride != b.stride || a.stride == 0) return true;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const size_t d = (size_t)((b0 >= a0 ? (b0 - a0) % a.stride : a.stride - (a0 - b0) % a.stride) % a.stride);
+  return d < a.width || d + b.width > a.stride;
+}
+
+inline svdq_status check_rows(const Rows& out, std::initializer_list<Rows> others) {
+  for (const Rows& o : others)
+    if (meet(out, o)) return fail(SVDQ_STATUS_INVALID_VALUE, "output %s overlaps %s", out.name, o.name);
+  return SVDQ_STATUS_SUCCESS;
+}
+
+inline bool bad_ptr(const void* p) { return p && !aligned16(p); }
+
+inline svdq_status launched(hipError_t e, const char* what) {
+  if (e != hipSuccess) return fail(SVDQ_STATUS_HIP_ERROR, "%s launch: %s", what, hipGetErrorString(e));
+  return ok();
+}
+
+constexpr int64_t kMaxRows = 1ll << 24;
 
 inline size_t sz(int64_t a, int64_t b = 1, int64_t c = 1) { return (size_t)a * (size_t)b * (size_t)c; }
 

@@ -4,7 +4,6 @@
 // before any HIP call, as in api.cpp.
 
 #include <cmath>
-#include <cstring>
 
 #include "api_checks.h"
 #include "svdq_internal.h"
@@ -13,35 +12,6 @@ namespace {
 
 using namespace svdq_api;
 
-constexpr int64_t kMaxRows = 1ll << 24;
-
-// rows of `width` bytes, `stride` bytes apart
-struct Rows {
-  const void* p;
-  size_t stride, width, rows;
-  const char* name;
-};
-
-size_t extent(const Rows& r) { return r.rows == 0 ? 0 : (r.rows - 1) * r.stride + r.width; }
-
-// Whether two sets of rows may share a byte.  Rows of one stride can interleave
-// (the Q and K columns of one projection's output): their places within a
-// stride decide.
-bool meet(const Rows& a, const Rows& b) {
-  if (!a.p || !b.p) return false;
-  if (!overlap({a.p, extent(a), a.name}, {b.p, extent(b), b.name})) return false;
-  if (a.stride != b.stride || a.stride == 0) return true;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  const size_t d = (size_t)((b0 >= a0 ? (b0 - a0) % a.stride : a.stride - (a0 - b0) % a.stride) % a.stride);
-  return d < a.width || d + b.width > a.stride;
-}
-
-svdq_status check_rows(const Rows& out, std::initializer_list<Rows> others) {
-  for (const Rows& o : others)
-    if (meet(out, o)) return fail(SVDQ_STATUS_INVALID_VALUE, "output %s overlaps %s", out.name, o.name);
-  return SVDQ_STATUS_SUCCESS;
-}
-
 // `in` as check_rows takes it, or nothing where its rows are exactly those of
 // `out`: an update in place, of an input that each thread reads at its own places
 // before it writes them
@@ -49,13 +19,6 @@ Rows unless_in_place(const Rows& out, const Rows& in) {
   const bool same = in.p == out.p && in.width == out.width && in.rows == out.rows &&
                     (in.stride == out.stride || in.rows == 1);
   return same ? Rows{} : in;
-}
-
-bool bad_ptr(const void* p) { return p && !aligned16(p); }
-
-svdq_status launched(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(SVDQ_STATUS_HIP_ERROR, "%s launch: %s", what, hipGetErrorString(e));
-  return ok();
 }
 
 svdq_status validate_w8a8(int64_t M, int64_t N, int64_t K) {
@@ -170,9 +133,9 @@ svdq_status svdq_gate_norm_modulate(const void* x, int stream_type, int64_t x_st
   for (int n : {post_norm, norm})
     if (n != SVDQ_NORM_NONE && n != SVDQ_NORM_LAYER && n != SVDQ_NORM_RMS)
       return fail(SVDQ_STATUS_INVALID_VALUE, "unknown norm %d", n);
-  if (out_type != SVDQ_NORM_OUT_BF16 && out_type != SVDQ_NORM_OUT_INT8)
+  if (out_type != SVDQ_NORM_OUT_BF16 && out_type != SVDQ_NORM_OUT_INT8 && out_type != SVDQ_NORM_OUT_FP8)
     return fail(SVDQ_STATUS_INVALID_VALUE, "unknown output type %d", out_type);
-  const bool q8 = out_type == SVDQ_NORM_OUT_INT8;
+  const bool q8 = out_type != SVDQ_NORM_OUT_BF16, fp8 = out_type == SVDQ_NORM_OUT_FP8;
   if (q8 && C % 64 != 0)
     return fail(SVDQ_STATUS_NOT_SUPPORTED, "C=%lld is not a multiple of 64 (8-bit output)", (long long)C);
   if (!std::isfinite(eps) || eps < 0.0f) return fail(SVDQ_STATUS_INVALID_VALUE, "eps must be finite and >= 0");
@@ -216,7 +179,7 @@ svdq_status svdq_gate_norm_modulate(const void* x, int stream_type, int64_t x_st
       rw{weight, 0, c * 2, 1, "weight"}, rsm{smooth, 0, c * 4, 1, "smooth"},
       rh{has_y ? h : nullptr, (size_t)h_stride * e, c * e, m, "h"},
       rz{has_z ? z : nullptr, c * (q8 ? 1 : 2), c * (q8 ? 1 : 2), m, "z"},
-      rzs{q8 ? z_scales : nullptr, 0, m * 4, 1, "z_scales"};
+      rzs{q8 ? z_scales : nullptr, 0, m * 4 * (fp8 ? (c + 127) / 128 : 1), 1, "z_scales"};
   // h may be x, and with it y, or a gate of M rows, where these are x too: a row's x,
   // y and gate are read before its h is written, scale and shift after it
   svdq_status s = SVDQ_STATUS_SUCCESS;
@@ -253,6 +216,7 @@ svdq_status svdq_gate_norm_modulate(const void* x, int stream_type, int64_t x_st
   a.post = post_norm;
   a.norm = norm;
   a.x_fp32 = stream_type == SVDQ_STREAM_FP32;
+  a.fp8 = fp8;
   a.alpha = residual_scale;
   a.eps = eps;
   return launched(svdq::launch_gate_norm(a, static_cast<hipStream_t>(stream)), "gate norm");

@@ -1,0 +1,627 @@
+// The 8-bit floating-point linear on gfx950:
+//   Y[m,n] = epi( sum_b s_x[b,m] s_w[n/128,b] (sum_{k in b} q_x[m,k] q_w[n,k]) + bias[n] )
+// over blocks b of 128 channels, e4m3 codes, and its gated form, two such products of
+// the same tokens, H = act(G) U, as bf16 or as the next linear's codes.
+//
+// A block is exactly the K of one v_mfma_f32_16x16x128_f8f6f4 (32 cycles, 2048 operations
+// a cycle and SIMD): every MFMA starts from zero and its four results per lane join the
+// fp32 sums by one fma each with the block's scale, 16 of the 32 cycles on the vector
+// unit.  With the weights as the A operand a lane's results belong to one token, so the
+// scale s_x s_w is one product per token tile and block, not one per result.
+//  * workgroup tile of WN x WM waves, each 32 H weight rows x 16 J token rows (256 x 256 on
+//    8 waves, H = J = 4: 128 fp32 sums per lane, two waves per SIMD); weight rows come in
+//    two halves, in the gated form G's and U's of the same features, so that H is
+//    formed in registers;
+//  * R LDS stages of 128 bytes per row, filled by global_load_lds_dwordx4; a row's
+//    granule g of 16 bytes sits at slot g ^ row[3:1] (bank conflicts: see
+//    w8a8_gemm.hip), token scales beside them.  A lane takes granules lq and lq + 4 of its
+//    rows: the order within a block does not matter as long as both operands have it;
+//  * a stage is computed in phases of 2 x J tiles.  While a phase's MFMAs run, the weight
+//    fragments of the next are read; in the last one, behind the stage's only barrier,
+//    the next stage's tokens take the places of this one's as they are used up, and
+//    the stage's LDS, read by all, is filled for stage q + R;
+//  * few tiles: K is split over workgroups, whose fp32 partials meet in the caller's
+//    workspace; the last to arrive adds them in the order of K, so that results do
+//    not depend on timing.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <type_traits>
+
+#include "fp8.h"
+#include "tile_device.h"
+
+namespace svdq {
+namespace {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void dma4(const void* gptr, uint8_t* lds_wave_base) {
+  __builtin_amdgcn_global_load_lds((glb_void*)gptr, (lds_void*)lds_wave_base, 4, 0, 0);
+}
+
+struct TileArgs {
+  Fp8Args g;
+  int splits;   // over K, gridDim.y
+  u32* count;   // one arrival counter per tile (splits > 1)
+  float* part;  // fp32 partials [tile][splits][waves][2 H J][64][4]
+};
+
+// WN x WM waves of 2 H x J tiles of 16 x 16, R stages in LDS
+template <int H, int J, int WN, int WM, int R>
+struct Shape {
+  static constexpr int kWaves = WN * WM, kThreads = 64 * kWaves;
+  static constexpr int kTN = 32 * H * WN, kTM = 16 * J * WM;
+  static constexpr int kTurn = 512 * H;  // bytes of 16 rows of a wave's columns on their way out
+  static constexpr int kLds = R * (128 * (kTN + kTM) + 4 * kTM) + kWaves * kTurn;
+  static_assert(kLds <= 160 * 1024 - 1024, "the stages and the rows of Y on their way fit the LDS");
+  static constexpr int kWgs = kLds > 79 * 1024 ? 1 : 2;  // per CU, by LDS
+};
+
+enum Form { kPlain, kGated, kGatedCodes };
+
+template <int H, int J, int WN, int WM, int R, Form kForm, bool kSplit>
+__global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_tile_kernel(const TileArgs p) {
+  using Sh = Shape<H, J, WN, WM, R>;
+  static_assert(R >= 2 && R <= 4, "stage buffers");
+  constexpr bool kGate = kForm != kPlain;
+  constexpr int kTN = Sh::kTN, kTM = Sh::kTM, kWaves = Sh::kWaves;
+  constexpr int kCols = kGate ? kTN / 2 : kTN;        // output columns of a tile
+  constexpr int kWaveCols = kGate ? 16 * H : 32 * H;  // and of a wave
+  // one LDS object per operand and stage, so the compiler sees that a DMA
+  // into one cannot alias reads of another
+  __shared__ __attribute__((aligned(16))) uint8_t w0[kTN * 128], w1[kTN * 128], a0[kTM * 128], a1[kTM * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t w2[R > 2 ? kTN * 128 : 16], a2[R > 2 ? kTM * 128 : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t w3[R > 3 ? kTN * 128 : 16], a3[R > 3 ? kTM * 128 : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t s0[kTM * 4], s1[kTM * 4], s2[R > 2 ? kTM * 4 : 16],
+      s3[R > 3 ? kTM * 4 : 16];
+  auto wbuf = [&](int b) -> uint8_t* { return b == 0 ? w0 : b == 1 ? w1 : b == 2 ? w2 : w3; };
+  auto abuf = [&](int b) -> uint8_t* { return b == 0 ? a0 : b == 1 ? a1 : b == 2 ? a2 : a3; };
+  auto sbuf = [&](int b) -> uint8_t* { return b == 0 ? s0 : b == 1 ? s1 : b == 2 ? s2 : s3; };
+  __shared__ __attribute__((aligned(16))) uint8_t rows[kWaves * Sh::kTurn];  // the epilogue's own
+  __shared__ float red[kForm == kGatedCodes ? kWaves * 16 * J : 1];
+  __shared__ u32 arrived;
+
+  const int M = p.g.M, N = p.g.N, K = p.g.K;
+  const int tiles_n = (N + kCols - 1) / kCols;
+  const int S_all = (K + 127) >> 7;  // stages; the last one may be half (K % 128 == 64)
+  const int q_begin = kSplit ? (int)((long)blockIdx.y * S_all / p.splits) : 0;
+  const int q_end = kSplit ? (int)((long)(blockIdx.y + 1) * S_all / p.splits) : S_all;
+  const int S = q_end - q_begin;
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave / WM;
+  const int wm = wave % WM;
+  const int l16 = lane & 15;
+  const int lq = lane >> 4;
+  int tm, tn;
+  tile_of(blockIdx.x, (M + kTM - 1) / kTM, tiles_n, tm, tn);
+  const int n0 = tn * kCols, m0 = tm * kTM;
+
+  // Weight scales of the wave's two halves, one of each a stage, by scalar loads (as
+  // constant memory: nothing writes them during the launch) a stage ahead
+  typedef const float __attribute__((address_space(4))) cfloat;
+  const int blocks_n = (N + 127) >> 7;
+  const size_t ws_at = (size_t)min((n0 + wn * kWaveCols) >> 7, blocks_n - 1) * S_all + q_begin;
+  cfloat* ws0 = (cfloat*)(p.g.w_scales + ws_at);
+  cfloat* ws1 = (cfloat*)((kGate ? p.g.up_scales : p.g.w_scales) + ws_at);
+  float sw0, sw1;
+  // the half stage sums its 64 products twice (below)
+  const int half_at = q_end == S_all && (K & 64) != 0 ? S - 1 : S;
+  auto load_ws = [&](int q) {
+    const int at = min(q, S - 1);
+    sw0 = ws0[at];
+    if constexpr (kGate) sw1 = ws1[at];
+  };
+  load_ws(0);
+
+  // DMA role: instruction k of a wave fills rows 8 (waves k + wave) + lane / 8, slot
+  // lane % 8 of each row, with granule (lane % 8) ^ row[3:1].  Rows past the
+  // end repeat the last row (never stored).  In a half stage the granules of
+  // the missing half repeat those of the first, in both operands: the sum is twice that of
+  // the 64 products, its scale is halved.
+  const u32 gran = 16u * (u32)((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));
+  const u32 back = (K & 64) != 0 && gran >= 64 ? 64u : 0u;
+  constexpr int kWd = kTN / (8 * kWaves), kAd = kTM / (8 * kWaves);  // DMAs per stage and wave
+  constexpr int kDmas = kWd + kAd + 1;                               // and one of the token scales
+  static_assert(kWaves % 2 == 0 && kWd * 8 * kWaves == kTN && kAd * 8 * kWaves == kTM, "whole row runs per wave");
+  static_assert(kTM % 64 == 0 && kTM <= 64 * kWaves, "the waves cover the token scales");
+  const u32 wlane = (u32)(lane >> 3) * (u32)K + gran;
+  const uint8_t* abase = p.g.act + (size_t)m0 * (size_t)K;
+  const uint8_t* wbase[kWd];
+  u32 aoff[kAd];
+  // (N % 64 == 0: the 8 weight rows of an instruction are all inside or all
+  // past the end, so their address is uniform)
+#pragma unroll
+  for (int k = 0; k < kWd; ++k) {
+    const int row = 8 * (kWaves * k + wave);
+    if constexpr (kGate) {
+      // a wave's 32 H rows of LDS: G's 16 H features, then U's
+      const int in = row % (32 * H);
+      const int f = (row / (32 * H)) * 16 * H + in % (16 * H);
+      wbase[k] = (in >= 16 * H ? p.g.up : p.g.w) + (size_t)min(n0 + f, N - 8) * (size_t)K;
+    } else {
+      wbase[k] = p.g.w + (size_t)min(n0 + row, N - 8) * (size_t)K;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kAd; ++k)
+    aoff[k] = (u32)(min(m0 + 8 * (kWaves * k + wave) + (lane >> 3), M - 1) - m0) * (u32)K + gran;
+  const int srow = 64 * (wave % (kTM / 64));  // the wave's run of token scales
+  const u32 soff = 4u * (u32)(min(m0 + srow + lane, M - 1) - m0);
+  const uint8_t* sbase = reinterpret_cast<const uint8_t*>(p.g.act_scales + m0);
+  struct Col {
+    u32 x, back;
+    const uint8_t* s;
+  };
+  // column of stage q (counted from q_begin; past the end the last stage again)
+  auto stage_col = [&](int q) {
+    const int s = min(q_begin + q, q_end - 1);
+    return Col{128u * (u32)s, s == S_all - 1 ? back : 0u, sbase + 4 * (size_t)s * (size_t)p.g.act_stride};
+  };
+  auto dma_one = [&](int k, const Col& col, auto bc) {
+    constexpr int b = decltype(bc)::value;
+    if (k < kWd) dma16(wbase[k] + col.x + (wlane - col.back), wbuf(b) + 1024 * (kWaves * k + wave));
+    else if (k < kWd + kAd)
+      dma16(abase + col.x + (aoff[k - kWd] - col.back), abuf(b) + 1024 * (kWaves * (k - kWd) + wave));
+    else dma4(col.s + soff, sbuf(b) + 4 * srow);
+  };
+  auto dma_stage = [&](int q, auto bc) {
+    const Col col = stage_col(q);
+#pragma unroll
+    for (int k = 0; k < kDmas; ++k) dma_one(k, col, bc);
+  };
+
+  // Fragments: lane (l16, lq) takes granules lq and lq + 4 of row 16 i + l16.
+  constexpr int kG = H > 1 ? 2 : 1;       // weight tiles of a phase
+  constexpr int kP = 2 * H / kG;          // phases of a stage; the first half of them is the first half of the rows
+  constexpr int kSlots = kG * J;          // MFMAs of a phase
+  const int fo = 128 * l16 + 16 * (lq ^ (l16 >> 1));
+  const int wrow = wn * 32 * H * 128, arow = wm * 16 * J * 128;
+  v8i fw[2][kG], fa[J];
+  float st[J];
+  auto read_tile = [&](const uint8_t* t) {
+    const v4i lo = *reinterpret_cast<const v4i*>(t + fo), hi = *reinterpret_cast<const v4i*>(t + (fo ^ 64));
+    return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  auto read_w = [&](auto bc, int i) { return read_tile(wbuf(decltype(bc)::value) + wrow + 2048 * i); };
+  auto read_a = [&](auto bc, int j) { return read_tile(abuf(decltype(bc)::value) + arow + 2048 * j); };
+  auto read_s = [&](auto bc, int j) {
+    return *reinterpret_cast<const float*>(sbuf(decltype(bc)::value) + 4 * (wm * 16 * J + 16 * j + l16));
+  };
+
+  v4f acc[2 * H][J];
+#pragma unroll
+  for (int i = 0; i < 2 * H; ++i)
+#pragma unroll
+    for (int j = 0; j < J; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  // MFMA results join their sums kLag slots later
+  constexpr int kLag = kSlots >= 4 ? 4 : 2;
+  v4f pend[kLag];
+  float pend_c[kLag];
+#pragma unroll
+  for (int t = 0; t < kLag; ++t) pend[t] = v4f{0.f, 0.f, 0.f, 0.f}, pend_c[t] = 0.f;
+  auto join = [&](v4f& s, const v4f& d, float c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = __builtin_fmaf(d[e], c, s[e]);
+  };
+  // slot t of phase ph: the MFMA of weight tile t % kG and token tile t / kG; the results of
+  // the MFMA kLag slots before it are added
+  auto slot = [&](int ph, int t, const v8i& w, const v8i& a, float c) {
+    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+    const v4f d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, zero, 0, 0, 0, 0, 0, 0);
+    const int was = t >= kLag ? ph : (ph + kP - 1) % kP, at = t >= kLag ? t - kLag : kSlots + t - kLag;
+    join(acc[kG * was + at % kG][at / kG], pend[t % kLag], pend_c[t % kLag]);
+    pend[t % kLag] = d;
+    pend_c[t % kLag] = c;
+  };
+  static_assert(kSlots % kLag == 0, "the places of what is pending are those of the slots");
+
+  using B0 = std::integral_constant<int, 0>;
+  using B1 = std::integral_constant<int, 1>;
+  using B2 = std::integral_constant<int, 2>;
+  using B3 = std::integral_constant<int, 3>;
+  float c[J];
+  auto scales_of = [&](float sw) {
+#pragma unroll
+    for (int j = 0; j < J; ++j) c[j] = st[j] * sw;
+  };
+  // stage q from buffer bc: its tokens, its token scales and the first phase's weights
+  // are in registers
+  auto iteration = [&](int q, auto bc) {
+    constexpr int b = decltype(bc)::value;
+    using BC = std::integral_constant<int, b>;
+    using BN = std::integral_constant<int, (b + 1) % R>;
+    const float half = q == half_at ? 0.5f : 1.0f, up = kGate ? half * sw1 : 0.f;
+    scales_of(half * sw0);
+#pragma unroll
+    for (int ph = 0; ph < kP; ++ph) {
+      if (kGate && ph == kP / 2) scales_of(up);
+      if (ph == kP - 2) load_ws(q + 1);
+      if (ph < kP - 1) {
+#pragma unroll
+        for (int t = 0; t < kSlots; ++t) {
+          __builtin_amdgcn_sched_barrier(0);
+          slot(ph, t, fw[ph & 1][t % kG], fa[t / kG], c[t / kG]);
+          if (t < kG) fw[(ph + 1) & 1][t] = read_w(BC{}, kG * (ph + 1) + t);
+        }
+      } else {
+        const Col col = stage_col(q + R);
+        __builtin_amdgcn_sched_barrier(0);
+        // this wave's reads of the stage, and its DMAs of the next one; those of
+        // the R - 2 stages after it may still be in flight
+        wait_vm_lds<(R - 2) * kDmas>();
+        barrier();
+        static_assert(kP % 2 == 0, "the next stage's first phase takes the other weight registers");
+#pragma unroll
+        for (int t = 0; t < kSlots; ++t) {
+          __builtin_amdgcn_sched_barrier(0);
+          slot(ph, t, fw[ph & 1][t % kG], fa[t / kG], c[t / kG]);
+          if (t == 0) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) st[j] = read_s(BN{}, j);
+          }
+          if (t < kG) fw[0][t] = read_w(BN{}, t);
+          if (t % kG == kG - 1) fa[t / kG] = read_a(BN{}, t / kG);
+          constexpr int kEach = (kDmas + kSlots - 1) / kSlots;
+#pragma unroll
+          for (int k = kEach * t; k < kEach * (t + 1) && k < kDmas; ++k) dma_one(k, col, BC{});
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  dma_stage(0, B0{});
+  dma_stage(1, B1{});
+  if constexpr (R > 2) dma_stage(2, B2{});
+  if constexpr (R > 3) dma_stage(3, B3{});
+  wait_vm_lds<(R - 1) * kDmas>();
+  barrier();
+#pragma unroll
+  for (int t = 0; t < kG; ++t) fw[0][t] = read_w(B0{}, t);
+#pragma unroll
+  for (int j = 0; j < J; ++j) fa[j] = read_a(B0{}, j), st[j] = read_s(B0{}, j);
+
+  int q = 0;
+  for (; q + R <= S; q += R) {
+    iteration(q, B0{});
+    iteration(q + 1, B1{});
+    if constexpr (R > 2) iteration(q + 2, B2{});
+    if constexpr (R > 3) iteration(q + 3, B3{});
+  }
+  if (q < S) iteration(q, B0{});
+  if constexpr (R > 2)
+    if (q + 1 < S) iteration(q + 1, B1{});
+  if constexpr (R > 3)
+    if (q + 2 < S) iteration(q + 2, B2{});
+#pragma unroll
+  for (int t = 0; t < kLag; ++t) {
+    const int at = kSlots + t - kLag;
+    join(acc[kG * (kP - 1) + at % kG][at / kG], pend[t], pend_c[t]);
+  }
+  wait_vm_lds<0>();  // no DMA may land in the LDS that the epilogue or a next workgroup takes
+
+  if constexpr (kSplit) {
+    // Every workgroup stores its fp32 sums with agent-coherent stores, waits for them and
+    // bumps the tile's counter (which wraps to zero); the last to arrive adds all of them
+    // in the order of K.
+    typedef unsigned long long u64;
+    constexpr int kWg = Sh::kWaves * 2 * H * J * 256;
+    float* part = p.part + (size_t)blockIdx.x * p.splits * kWg + (size_t)wave * (2 * H * J * 256) + 4 * lane;
+    u64* mine = reinterpret_cast<u64*>(part + (size_t)blockIdx.y * kWg);
+    typedef float v2f __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 2 * H; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          __hip_atomic_store(mine + 128 * (i * J + j) + e,
+                             __builtin_bit_cast(u64, v2f{acc[i][j][2 * e], acc[i][j][2 * e + 1]}), __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+    wait_vm_lds<0>();  // the partial is visible to the agent
+    barrier();
+    if (tid == 0) arrived = atomicInc(p.count + blockIdx.x, (u32)(p.splits - 1));
+    __syncthreads();
+    if (arrived != (u32)(p.splits - 1)) return;
+    __asm__ volatile("" ::: "memory");
+    for (int s = 0; s < p.splits; ++s) {
+      const u64* src = reinterpret_cast<const u64*>(part + (size_t)s * kWg);
+#pragma unroll
+      for (int i = 0; i < 2 * H; ++i) {
+        u64 t[J][2];
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            t[j][e] = __hip_atomic_load(src + 128 * (i * J + j) + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const v2f v = __builtin_bit_cast(v2f, t[j][e]);
+            acc[i][j][2 * e] = s == 0 ? v[0] : acc[i][j][2 * e] + v[0];
+            acc[i][j][2 * e + 1] = s == 0 ? v[1] : acc[i][j][2 * e + 1] + v[1];
+          }
+      }
+    }
+  }
+
+  // The epilogue, in fp32 from the sums.  A wave turns its tile 16 token rows at a time
+  // through LDS of its own, so that rows leave in runs of 16 bytes per lane.
+  int el = lane;
+  __asm__ volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(el));
+  const int e16 = el & 15, eq = el >> 4;
+  uint8_t* turn = rows + wave * Sh::kTurn;
+  const int nw = n0 + wn * kWaveCols, mw = m0 + wm * 16 * J;  // the wave's first column and row
+  auto bias4 = [&](const uint16_t* b, int n, float (&f)[4]) {
+    const uint2 v = b != nullptr ? *reinterpret_cast<const uint2*>(b + min(n, N - 4)) : uint2{0u, 0u};
+    f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
+  };
+  if constexpr (kGate) {
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      const int n = nw + 16 * i + 4 * eq;
+      float bg[4], bu[4];
+      bias4(p.g.bias, n, bg);
+      bias4(p.g.up_bias, n, bu);
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[i][j][e] = gate_act(acc[i][j][e] + bg[e], p.g.epilogue) * (acc[H + i][j][e] + bu[e]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2 * H; ++i) {
+      float b[4];
+      bias4(p.g.bias, nw + 16 * i + 4 * eq, b);
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float o = acc[i][j][e] + b[e];
+          acc[i][j][e] = p.g.epilogue == kEpilogueGelu ? gelu_exp2(o) : o;
+        }
+    }
+  }
+  if constexpr (kForm == kGatedCodes) {
+    // a token's block of 128 features lies in the WN waves of a tile row: their
+    // maxima meet in LDS.  Features past the end (a half last block) are whole waves'
+    static_assert(kCols == 128, "a tile holds a block of features");
+    const bool in = nw < N;
+    if (p.g.smooth != nullptr) {
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const float4 s = *reinterpret_cast<const float4*>(p.g.smooth + min(nw + 16 * i + 4 * eq, N - 4));
+        const float mu[4] = {1.0f / s.x, 1.0f / s.y, 1.0f / s.z, 1.0f / s.w};
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] *= mu[e];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < H; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = BitMaxOp::run(m, __builtin_fabsf(acc[i][j][e]));
+      m = max_rows4(in ? m : 0.f);
+      if (eq == 0) red[(wn * WM + wm) * 16 * J + 16 * j + e16] = m;
+    }
+    __syncthreads();
+    if (!in) return;
+    constexpr int kRow = 16 * H;  // bytes of a row of the wave's codes
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      float m = red[wm * 16 * J + 16 * j + e16];
+#pragma unroll
+      for (int w = 1; w < WN; ++w) m = BitMaxOp::run(m, red[(w * WM + wm) * 16 * J + 16 * j + e16]);
+      float s, inv;
+      block_scale(m, s, inv);
+      const int tok = mw + 16 * j + e16;
+      if (wn == 0 && eq == 0 && tok < M) p.g.out_scales[(size_t)tn * p.g.out_stride + tok] = s;
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        const u32 q4 = fp8_codes4(v, inv);
+        *reinterpret_cast<u32*>(turn + e16 * kRow + 16 * (i ^ ((e16 >> 1) & (H - 1))) + 4 * eq) = inv == 0.f ? 0u : q4;
+      }
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes are done
+      __asm__ volatile("" ::: "memory");
+      const int ml = el / H, ch = el - ml * H;
+      const int m2 = mw + 16 * j + ml;
+      if (el < 16 * H) {
+        const v4u v = *reinterpret_cast<const v4u*>(turn + ml * kRow + 16 * (ch ^ ((ml >> 1) & (H - 1))));
+        if (m2 < M) *reinterpret_cast<v4u*>(static_cast<uint8_t*>(p.g.out) + (size_t)m2 * N + nw + 16 * ch) = v;
+      }
+      __asm__ volatile("" ::: "memory");  // (a wave's LDS operations run in order)
+    }
+  } else {
+    // bf16 rows, 16 H columns of a half at a time
+    constexpr int kChunks = 2 * H, kMask = kChunks - 1;  // 16-byte chunk c of row m sits at c ^ (m & kMask)
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int h = 0; h < (kGate ? 1 : 2); ++h) {
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+          const v4f& o = acc[h * H + i][j];
+          const int nl = 16 * i + 4 * eq;
+          uint8_t* dst = turn + e16 * (16 * kChunks) + (((nl >> 3) ^ (e16 & kMask)) << 4) + 8 * (eq & 1);
+          *reinterpret_cast<uint2*>(dst) = uint2{pack2_bf16(o[0], o[1]), pack2_bf16(o[2], o[3])};
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's LDS writes are done
+        __asm__ volatile("" ::: "memory");
+#pragma unroll
+        for (int t = 0; t < (H + 1) / 2; ++t) {
+          const int at = 64 * t + el;
+          const int ml = at / kChunks, ch = at - ml * kChunks;
+          const int m = mw + 16 * j + ml, n = nw + h * 16 * H + 8 * ch;
+          if (at < 16 * kChunks) {
+            const v4u v = *reinterpret_cast<const v4u*>(turn + ml * (16 * kChunks) + ((ch ^ (ml & kMask)) << 4));
+            // N % 64 == 0, so n < N covers n + 7
+            if (m < M && n < N)
+              __builtin_nontemporal_store(v, reinterpret_cast<v4u*>(static_cast<uint16_t*>(p.g.out) + (size_t)m * N + n));
+          }
+        }
+        __asm__ volatile("" ::: "memory");  // (a wave's LDS operations run in order)
+      }
+  }
+}
+
+struct Plan {
+  int shape;    // index into kShapes
+  int tiles;
+  int splits;
+  double cost;  // us, by the model below
+};
+
+// Workgroup tiles, the test hook's name of each (weight rows / 64, tokens / 64, LDS stages)
+// and what a launch takes by the model of w8a8_gemm.hip: base + n (fill + S step) us with n
+// workgroups on the busiest compute unit and S stages of 128 k, pairs of workgroups at fill2
+// and step2 where two share a compute unit.
+#define SVDQ_SHAPES(X)                                   \
+  X(442, 4, 4, 2, 4, 2, -3.29, 11.18, 1.25, 0.0, 0.0)    \
+  X(423, 2, 4, 4, 2, 3, -1.0, 8.0, 0.70, 0.0, 0.0)       \
+  X(413, 2, 2, 4, 2, 3, 1.0, 5.0, 0.45, 0.0, 0.0)        \
+  X(224, 2, 4, 2, 2, 4, 1.06, 4.89, 0.45, 0.0, 0.0)      \
+  X(213, 2, 2, 2, 2, 3, 2.0, 2.83, 0.26, 3.5, 0.45)      \
+  X(114, 1, 2, 2, 2, 4, 3.00, 1.45, 0.18, 2.07, 0.365)
+struct ShapeInfo {
+  int code, tn, tm, waves, wgs;
+  double base, fill, step, fill2, step2;
+};
+template <int H, int J, int WN, int WM, int R>
+constexpr ShapeInfo info(int code, double base, double fill, double step, double fill2, double step2) {
+  using S = Shape<H, J, WN, WM, R>;
+  return ShapeInfo{code, S::kTN, S::kTM, S::kWaves, S::kWgs, base, fill, step, fill2, step2};
+}
+#define SVDQ_INFO(code, h, j, wn, wm, r, base, fill, step, fill2, step2) \
+  info<h, j, wn, wm, r>(code, base, fill, step, fill2, step2),
+constexpr ShapeInfo kShapes[] = {SVDQ_SHAPES(SVDQ_INFO)};
+#undef SVDQ_INFO
+constexpr int kMaxSplits = 16;
+
+std::atomic<int> g_tile{0}, g_splits{0};  // test hook
+
+Form form_of(const Fp8Args& a) { return a.up == nullptr ? kPlain : a.out_scales == nullptr ? kGated : kGatedCodes; }
+
+int64_t tiles_of(const ShapeInfo& s, const Fp8Args& a) {
+  const int64_t cols = a.up != nullptr ? s.tn / 2 : s.tn;
+  return ((a.N + cols - 1) / cols) * (((int64_t)a.M + s.tm - 1) / s.tm);
+}
+
+// the cheapest tile and K-split
+Plan plan_of(const Fp8Args& a) {
+  const int cus = current_cus();
+  const int stages = (a.K + 127) / 128;
+  const Form form = form_of(a);
+  const int forced_tile = g_tile.load(std::memory_order_relaxed), forced = g_splits.load(std::memory_order_relaxed);
+  Plan best{-1, 0, 1, 0.0};
+  for (int i = 0; i < (int)(sizeof(kShapes) / sizeof(kShapes[0])); ++i) {
+    const ShapeInfo& s = kShapes[i];
+    if (form == kGatedCodes && s.tn != 256) continue;  // a tile holds a block of features
+    if (forced_tile > 1 && forced_tile != s.code && !(form == kGatedCodes && forced_tile / 100 != 4)) continue;
+    const int64_t tiles = tiles_of(s, a);
+    if (tiles * s.waves * 64 >= (1ll << 32)) continue;  // a launch holds fewer than 2^32 threads
+    for (int splits = 1; splits <= std::min(kMaxSplits, stages); splits *= 2) {
+      const int64_t wgs = tiles * splits;
+      if (splits > 1 && tiles > (int64_t)kWsMaxCounters) break;
+      if (forced > 0 ? splits > forced : splits > 1 && wgs > 2 * cus) break;
+      const double n = (double)((wgs + cus - 1) / cus), S = (double)((stages + splits - 1) / splits);
+      double cost = s.base;
+      if (s.wgs == 2) {
+        const double pairs = std::floor(n / 2);
+        cost += pairs * (s.fill2 + S * s.step2) + (n - 2 * pairs) * (s.fill + S * s.step);
+      } else {
+        cost += n * (s.fill + S * s.step);
+      }
+      if (splits > 1) cost += 2.54 + 0.52 * splits + 0.57 * (s.tn / 64) * (s.tm / 64);  // the partials' round trips
+      if (best.shape < 0 || cost < best.cost || (forced > 0 && best.shape == i)) best = Plan{i, (int)tiles, splits, cost};
+    }
+  }
+  return best;
+}
+
+template <int H, int J, int WN, int WM, int R, Form kForm>
+void tile_form(const TileArgs& t, int tiles, hipStream_t stream) {
+  using Sh = Shape<H, J, WN, WM, R>;
+  const dim3 block(Sh::kThreads);
+  if (t.splits > 1)
+    hipLaunchKernelGGL((fp8_tile_kernel<H, J, WN, WM, R, kForm, true>), dim3(tiles, t.splits), block, 0, stream, t);
+  else
+    hipLaunchKernelGGL((fp8_tile_kernel<H, J, WN, WM, R, kForm, false>), dim3(tiles), block, 0, stream, t);
+}
+
+template <int H, int J, int WN, int WM, int R>
+hipError_t tile_go(const TileArgs& t, int tiles, hipStream_t stream) {
+  switch (form_of(t.g)) {
+    case kPlain: tile_form<H, J, WN, WM, R, kPlain>(t, tiles, stream); break;
+    case kGated: tile_form<H, J, WN, WM, R, kGated>(t, tiles, stream); break;
+    case kGatedCodes:
+      if constexpr (Shape<H, J, WN, WM, R>::kTN == 256) tile_form<H, J, WN, WM, R, kGatedCodes>(t, tiles, stream);
+      else return hipErrorInvalidValue;
+      break;
+  }
+  return hipGetLastError();
+}
+
+// The weight-streaming kernel for up to 16 tokens
+bool few_tokens(const Fp8Args& a) {
+  const int t = g_tile.load(std::memory_order_relaxed);
+  return t <= 1 && a.M <= 16;
+}
+
+size_t plan_bytes(const Plan& p) {
+  if (p.splits <= 1) return 0;
+  const ShapeInfo& s = kShapes[p.shape];
+  return ws_bytes((size_t)p.tiles, (size_t)p.tiles * p.splits * s.tn * s.tm * sizeof(float));
+}
+
+}  // namespace
+
+bool fp8_tile_known(int tile) {
+  if (tile == 0 || tile == 1) return true;
+  for (const ShapeInfo& s : kShapes)
+    if (s.code == tile) return true;
+  return false;
+}
+
+void set_fp8_plan_override(int tile, int splits) {
+  g_tile.store(tile, std::memory_order_relaxed);
+  g_splits.store(splits, std::memory_order_relaxed);
+}
+
+size_t fp8_workspace_bytes(const Fp8Args& a) {
+  return few_tokens(a) ? fp8_skinny_workspace_bytes(a) : plan_bytes(plan_of(a));
+}
+
+hipError_t launch_fp8_gemm(const Fp8Args& a, Workspace ws, hipStream_t stream) {
+  if (few_tokens(a)) return launch_fp8_skinny(a, ws, stream);
+  const Plan p = plan_of(a);
+  if (p.shape < 0 || plan_bytes(p) > ws.bytes) return hipErrorInvalidValue;
+  TileArgs t{a, p.splits, nullptr, nullptr};
+  if (p.splits > 1) {
+    t.count = ws_counters(ws);
+    t.part = static_cast<float*>(ws_scratch(ws));
+  }
+  switch (kShapes[p.shape].code) {
+#define SVDQ_GO(code, h, j, wn, wm, r, base, fill, step, fill2, step2) \
+  case code: return tile_go<h, j, wn, wm, r>(t, p.tiles, stream);
+    SVDQ_SHAPES(SVDQ_GO)
+#undef SVDQ_GO
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace svdq

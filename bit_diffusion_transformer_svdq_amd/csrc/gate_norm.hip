@@ -6,8 +6,9 @@
 //   z = norm(h) * w * (1 + scale) + shift
 //
 // in fp32 from the unrounded h; h is rounded once to the residual stream's type,
-// z once to bf16, or z goes straight to 8-bit codes with one scale per row, as
-// the 8-bit linear reads it.  Adaptive-normalization blocks of a diffusion
+// z once to bf16, or z goes straight to 8-bit codes: integers with one scale per row, or
+// e4m3 with one per row and 128 channels, as the 8-bit linears read them.
+// Adaptive-normalization blocks of a diffusion
 // transformer take gate, scale and shift from the modulation projections
 // (mind-verse.de, "Effiziente Optimierung von Diffusionsmodellen durch Nunchaku
 // 4-Bit-Quantisierung", section "Nunchaku Lite: Nahtlose Integration in
@@ -31,10 +32,13 @@
 
 #include <algorithm>
 
-#include "row_device.h"
+#include "fp8.h"
 
 namespace svdq {
 namespace {
+
+// what z leaves as
+enum NormOut { kOutBf16, kOutInt8, kOutFp8 };
 
 constexpr int kWgWaves1 = 4;  // rows (waves) per workgroup when one wave owns a row
 
@@ -81,7 +85,7 @@ struct Stream8 {
   }
 };
 
-template <int W, int V, bool F32, bool Q8>
+template <int W, int V, bool F32, NormOut kOut>
 __global__ __launch_bounds__(threads_of<W>()) void gate_norm_kernel(const GateNormArgs a) {
   __shared__ float red_all[W > 1 ? 10 * W : 1];  // two sets of reduction slots, rows take turns
   const int row0 = first_row<W>(a.run), row_end = min(row0 + a.run, a.M);
@@ -102,7 +106,7 @@ __global__ __launch_bounds__(threads_of<W>()) void gate_norm_kernel(const GateNo
   // fills them (16 waves, more than 8192 channels).  With one vector per lane (few
   // rows) they are taken behind the first row's loads (64 x 3072 5.1 -> 4.6 us),
   // with more ahead of the rows (4608 x 3072 25.7 -> 25.0 us)
-  constexpr bool kKeep = Q8 && (W < 16 || V == 1);
+  constexpr bool kKeep = kOut != kOutBf16 && (W < 16 || V == 1);
   float mu[kKeep ? V : 1][8];
   if constexpr (kKeep) {
     if (a.smooth != nullptr) {
@@ -245,7 +249,7 @@ __global__ __launch_bounds__(threads_of<W>()) void gate_norm_kernel(const GateNo
       }
     }
     const size_t zo = (size_t)row * a.C;
-    if constexpr (!Q8) {
+    if constexpr (kOut == kOutBf16) {
       uint16_t* z = static_cast<uint16_t*>(a.z) + zo;
 #pragma unroll
       for (int v = 0; v < V; ++v)
@@ -267,12 +271,24 @@ __global__ __launch_bounds__(threads_of<W>()) void gate_norm_kernel(const GateNo
 #pragma unroll
           for (int e = 0; e < 8; ++e) h[v][e] *= m[e];
         }
+        if constexpr (kOut == kOutFp8) amax = 0.f;  // of the lane's block of 128 channels, 16 lanes of one vector
         // (a lane past the row may hold what an update in place has already
         // written there: it takes no part)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           amax = (v < V - 1 || live) ? BitMaxOp::run(amax, __builtin_fabsf(h[v][e])) : amax;
+        if constexpr (kOut == kOutFp8) {
+          float s, inv;
+          block_scale(max16(amax), s, inv);
+          row_v2u c = {fp8_codes4(&h[v][0], inv), fp8_codes4(&h[v][4], inv)};
+          if (inv == 0.f) c = row_v2u{0u, 0u};
+          if (v < V - 1 || live) {
+            *reinterpret_cast<row_v2u*>(static_cast<uint8_t*>(a.z) + zo + off[v]) = c;
+            if ((lane0 & 15) == 0) a.scales[(size_t)(off[v] / kFp8Block) * a.M + row] = s;
+          }
+        }
       }
+      if constexpr (kOut == kOutFp8) continue;
       amax = row_reduce<BitMaxOp, W>(amax, red, 4);
       float s, inv;
       token_scale(amax, s, inv);
@@ -360,16 +376,18 @@ dim3 grid_of(int M, int run) {
   return dim3(W == 1 ? (owners + kWgWaves1 - 1) / kWgWaves1 : owners);
 }
 
-template <int W, int V, bool Q8>
+template <int W, int V, NormOut kOut>
 void gate_norm_go(const GateNormArgs& a, hipStream_t stream) {
   const dim3 grid = grid_of<W>(a.M, a.run), block(threads_of<W>());
-  if (a.x_fp32) hipLaunchKernelGGL((gate_norm_kernel<W, V, true, Q8>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((gate_norm_kernel<W, V, false, Q8>), grid, block, 0, stream, a);
+  if (a.x_fp32) hipLaunchKernelGGL((gate_norm_kernel<W, V, true, kOut>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((gate_norm_kernel<W, V, false, kOut>), grid, block, 0, stream, a);
 }
 template <int W, int V>
-void norm_bf16(const GateNormArgs& a, hipStream_t stream) { gate_norm_go<W, V, false>(a, stream); }
+void norm_bf16(const GateNormArgs& a, hipStream_t stream) { gate_norm_go<W, V, kOutBf16>(a, stream); }
 template <int W, int V>
-void norm_int8(const GateNormArgs& a, hipStream_t stream) { gate_norm_go<W, V, true>(a, stream); }
+void norm_int8(const GateNormArgs& a, hipStream_t stream) { gate_norm_go<W, V, kOutInt8>(a, stream); }
+template <int W, int V>
+void norm_fp8(const GateNormArgs& a, hipStream_t stream) { gate_norm_go<W, V, kOutFp8>(a, stream); }
 
 template <int W, int V, bool kSmooth>
 void quant_go(const QuantInt8Args& a, hipStream_t stream) {
@@ -426,7 +444,17 @@ hipError_t launch_gate_norm(const GateNormArgs& args, hipStream_t stream) {
   const int c8 = a.C >> 3, w = waves_for(a.M, c8, q8 ? kNormInt8PerLane : kNormPerLane);
   const int v = (c8 + 64 * w - 1) / (64 * w);
   a.run = run_for(a.M, w, a.smooth != nullptr);
-  if (q8) {
+  if (q8 && a.fp8) {
+    switch (16 * w + v) {
+      SVDQ_TO2(norm_fp8, 1)
+      SVDQ_TO2(norm_fp8, 2)
+      SVDQ_TO2(norm_fp8, 4)
+      SVDQ_TO2(norm_fp8, 8)
+      SVDQ_TO3(norm_fp8, 16)
+      SVDQ_AT(norm_fp8, 16, 4)
+      default: return hipErrorInvalidValue;
+    }
+  } else if (q8) {
     switch (16 * w + v) {
       SVDQ_TO2(norm_int8, 1)
       SVDQ_TO2(norm_int8, 2)

@@ -549,6 +549,22 @@ void parallel_rows(int64_t n, F f) {
   for (auto& x : th) x.join();
 }
 
+// the e4m3 code nearest to v (ties to the even code), at most 448 in magnitude: three
+// bits after the leading one from 2^-6 on, steps of 2^-9 below
+uint8_t e4m3_bits(double v) {
+  const double a = std::min(std::fabs(v), 448.0);
+  int e = 0;
+  std::frexp(a, &e);  // a = f 2^e, f in [1/2, 1)
+  e = std::max(e - 1, -6);
+  int m = static_cast<int>(std::nearbyint(std::ldexp(a, 3 - e)));  // 0 .. 16 units of 2^(e - 3)
+  if (m == 16) {
+    m = 8;
+    ++e;
+  }
+  const int bits = m < 8 ? m : ((e + 7) << 3) | (m - 8);
+  return static_cast<uint8_t>(bits | (std::signbit(v) ? 0x80 : 0));
+}
+
 }  // namespace
 
 extern "C" {
@@ -583,6 +599,43 @@ svdq_status svdq_pack_weights_int8(const uint16_t* w, const float* smooth, int64
         q[k] = static_cast<int8_t>(std::max(-127.0, std::min(127.0, t)));
       }
     }
+  });
+  if (!finite.load()) return svdq_internal_fail(SVDQ_STATUS_INVALID_VALUE, "a weight is not finite");
+  return svdq_internal_ok();
+}
+
+svdq_status svdq_pack_weights_fp8(const uint16_t* w, const float* smooth, int64_t N, int64_t K, uint8_t* w_codes,
+                                  float* w_scales) {
+  if (!w || !w_codes || !w_scales) return svdq_internal_fail(SVDQ_STATUS_INVALID_VALUE, "null pointer");
+  if (N <= 0 || K <= 0) return svdq_internal_fail(SVDQ_STATUS_INVALID_VALUE, "N and K must be positive");
+  const int64_t NB = (N - 1) / 128 + 1, KB = (K - 1) / 128 + 1;
+  std::atomic<bool> finite{true};
+  parallel_rows(NB, [&](int64_t a, int64_t b) {
+    for (int64_t nb = a; nb < b; ++nb)
+      for (int64_t kb = 0; kb < KB; ++kb) {
+        const int64_t n1 = std::min(N, 128 * (nb + 1)), k1 = std::min(K, 128 * (kb + 1));
+        auto value = [&](int64_t n, int64_t k) {
+          const double v = bf16_to_double(w[static_cast<size_t>(n) * K + k]);
+          return smooth ? v * static_cast<double>(smooth[k]) : v;
+        };
+        double top = 0.0;
+        bool good = true;
+        for (int64_t n = 128 * nb; n < n1; ++n)
+          for (int64_t k = 128 * kb; k < k1; ++k) {
+            const double v = std::fabs(value(n, k));
+            good = good && std::isfinite(v);
+            top = std::max(top, v);
+          }
+        const float s = static_cast<float>(top / 448.0);
+        if (!good || !std::isfinite(s)) {
+          finite.store(false);
+          return;
+        }
+        w_scales[nb * KB + kb] = s;
+        for (int64_t n = 128 * nb; n < n1; ++n)
+          for (int64_t k = 128 * kb; k < k1; ++k)
+            w_codes[static_cast<size_t>(n) * K + k] = s > 0.f ? e4m3_bits(value(n, k) / static_cast<double>(s)) : 0;
+      }
   });
   if (!finite.load()) return svdq_internal_fail(SVDQ_STATUS_INVALID_VALUE, "a weight is not finite");
   return svdq_internal_ok();

@@ -167,12 +167,13 @@ struct GateNormArgs {
   const uint16_t* shift;        // bf16 rows of C, or null
   const float* smooth;          // fp32 [C] or null (8-bit output only)
   void* h;                      // [M, C] of x's type (y given)
-  void* z;                      // bf16 [M, C], or int8 codes [M, C] (scales given)
-  float* scales;                // fp32 [M] or null
+  void* z;                      // bf16 [M, C], or codes [M, C] (scales given)
+  float* scales;                // fp32 [M], with fp8 [ceil(C / 128), M], or null
   int64_t x_stride, y_stride, h_stride, gate_stride, mod_stride;
   int M, C;
   int gate_every, mod_every;    // rows that share a gate row, a scale / shift row
   int post, norm, x_fp32;
+  int fp8;                      // codes are e4m3, not int8
   float alpha, eps;
   int run;                      // rows per workgroup, set by the launcher
 };
@@ -207,6 +208,48 @@ hipError_t launch_w8a8_gemm(const W8a8Args& a, Workspace ws, hipStream_t stream)
 // workgroup tiles; splits 0 by shape.
 bool w8a8_tile_known(int tile);
 void set_w8a8_plan_override(int tile, int splits);
+
+// The 8-bit floating-point linear: e4m3 codes, one fp32 scale for a token's (and a
+// weight tile's 128 rows') 128 channels of K; the last block of K may be 64 wide.
+constexpr int kActSilu = 0;
+constexpr int kActGelu = 1;
+
+// Per-token block quantization (quant_fp8.hip).  M > 0, K % 64 == 0, K <= kInt8MaxK.
+struct QuantFp8Args {
+  const uint16_t* x;     // bf16 [M, K]
+  const float* smooth;   // fp32 [K] or null
+  uint8_t* codes;        // [M, K]
+  float* scales;         // [ceil(K / 128)] rows of M, scale_stride apart
+  int64_t scale_stride;
+  int M, K;
+};
+hipError_t launch_quant_fp8(const QuantFp8Args& a, hipStream_t stream);
+
+// The product (fp8_gemm.hip, fp8_skinny.hip), plain or gated.  M > 0, N % 64 == 0,
+// K % 64 == 0, K <= kInt8MaxK.  Gated: w and up are the two projections, N features;
+// out is bf16 [M, N], or codes [M, N] with out_scales given.
+struct Fp8Args {
+  const uint8_t* act;       // codes [M, K]
+  const float* act_scales;  // [ceil(K / 128)] rows of M, act_stride apart
+  int64_t act_stride;
+  const uint8_t* w;         // codes [N, K]
+  const float* w_scales;    // [ceil(N / 128), ceil(K / 128)]
+  const uint8_t* up;        // as w, or null (plain)
+  const float* up_scales;
+  const uint16_t* bias;     // bf16 [N] or null
+  const uint16_t* up_bias;
+  const float* smooth;      // fp32 [N] or null (coded output only)
+  void* out;
+  float* out_scales;        // [ceil(N / 128)] rows of M, out_stride apart, or null
+  int64_t out_stride;
+  int M, N, K;
+  int epilogue;             // plain: kEpilogueNone / kEpilogueGelu; gated: kActSilu / kActGelu
+};
+size_t fp8_workspace_bytes(const Fp8Args& a);  // of the sizes; pointers only as null or not
+hipError_t launch_fp8_gemm(const Fp8Args& a, Workspace ws, hipStream_t stream);
+// Test hook, as set_w8a8_plan_override
+bool fp8_tile_known(int tile);
+void set_fp8_plan_override(int tile, int splits);
 
 // Rotary positions with several axes (rope_axes.hip).
 constexpr int kRopeMaxAngles = 128;  // R / 2

@@ -499,6 +499,85 @@ size_t svdq_w8a8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
 svdq_status svdq_debug_set_w8a8_plan(int tile, int splits);
 
 /*
+ * The 8-bit floating-point linear, for the projections and feed-forward blocks that are
+ * kept out of the 4-bit path (as the 8-bit linear above): e4m3 codes (the OCP 8-bit
+ * format: one sign, four exponent and three mantissa bits, largest value 448), one fp32
+ * scale for a token's 128 channels of K and one for 128 x 128 weights, so that an
+ * outlier coarsens its own block only.  KB = ceil(K / 128); the last block of K, and the
+ * last 128 rows of the weights, may be 64.
+ *
+ * svdq_quantize_act_fp8, per token m and block b:
+ *   x_hat = x, or with `smooth`  bf16(fl32(x * fl32(1/smooth)))
+ *   s     = fl32(max_{k in b} |x_hat| * fl32(1/448))
+ *   q     = e4m3(fl32(x_hat * fl32(1/s)))           (nearest, ties to even)
+ *   A block with fl32(1/s) not finite (all zero, or below about 1.3e-36) gets codes 0;
+ *   one that holds an infinity or NaN gets codes 0 and s = NaN, so that its token's
+ *   row of Y is NaN and no other row is touched.  Codes and scales are exactly
+ *   defined.
+ *   x device bf16 [M, K]; smooth device fp32 [K] or NULL
+ *   act_codes device out e4m3 [M, K]; act_scales device out fp32 [KB, M], one row per
+ *   block, rows act_scale_stride elements apart (>= M; a run of tokens is a run of each
+ *   row, so that a call can write or read part of a larger array; not read where KB = 1)
+ *
+ * svdq_fp8_gemm:
+ *   Y[m,n] = bf16( epi( sum_b fl32(s_x[b,m] s_w[n/128,b]) (sum_{k in b} q_x[m,k] q_w[n,k]) + bias[n] ) )
+ *   in fp32: a block's products are added by the matrix cores, one fma with its scale
+ *   adds it to the blocks before it; with few output tiles runs of blocks are added
+ *   on their own first.  (The matrix cores add e4m3 products eight neighbours at a time,
+ *   each cut off below 2^-13 of the power of two 2^r, r the largest sum of the two
+ *   codes' exponents among the eight; the groups' sums are fp32.)  Results are the
+ *   same in every run of a call.  epi none or
+ *   GELU (svdq_epilogue), one bf16 rounding.
+ *   act_codes, act_scales as above; w_codes e4m3 [N, K], w_scales fp32
+ *   [ceil(N / 128), KB] (svdq_pack_weights_fp8), bias bf16 [N] or NULL, y bf16 [M, N]
+ *   workspace of svdq_fp8_gemm_workspace_size(M, N, K) bytes (see Conventions)
+ *
+ * svdq_fp8_gated_gemm, both projections of a gated feed-forward block, the activation and
+ * the product in one kernel:
+ *   H[m,f] = act(G[m,f] + gate_bias[f]) * (U[m,f] + up_bias[f])
+ *   G and U the products of the same tokens with gate_codes and up_codes, e4m3 [F, K]
+ *   with scales fp32 [ceil(F / 128), KB]; biases bf16 [F] or NULL each; act SiLU,
+ *   v / (1 + exp(-v)), or GELU (tanh form).  (Values of act below 1e-36 in magnitude may
+ *   be -0.)  out: bf16 [M, F], or with SVDQ_GATED_OUT_FP8 the codes e4m3 [M, F] and
+ *   scales fp32 [ceil(F / 128), M] (rows out_scale_stride apart) that svdq_fp8_gemm reads:
+ *   those of svdq_quantize_act_fp8 for v = fl32(H fl32(1/smooth)) (smooth fp32 [F]), or H,
+ *   in fp32 in the place of x_hat, not rounded to bf16 in between.
+ *   workspace of svdq_fp8_gated_gemm_workspace_size(M, F, K, out_type) bytes
+ * K, N, F % 64 == 0, M <= 2^24, N, F <= 2^20, K <= 65536, strides <= 2^37 (NOT_SUPPORTED
+ * beyond); M == 0 is a no-op; INVALID_VALUE for an unknown enum value, smooth without
+ * 8-bit output, and as for the other calls.
+ */
+typedef enum { SVDQ_ACT_SILU = 0, SVDQ_ACT_GELU_TANH = 1 } svdq_activation;
+typedef enum { SVDQ_GATED_OUT_BF16 = 0, SVDQ_GATED_OUT_FP8 = 1 } svdq_gated_out;
+svdq_status svdq_quantize_act_fp8(const void* x, const float* smooth, int64_t M, int64_t K,
+                                  void* act_codes, float* act_scales, int64_t act_scale_stride, void* stream);
+svdq_status svdq_fp8_gemm(const void* act_codes, const float* act_scales, int64_t act_scale_stride,
+                          const void* w_codes, const float* w_scales, const void* bias,
+                          int64_t M, int64_t N, int64_t K, int epilogue, void* y,
+                          void* workspace, size_t workspace_bytes, void* stream);
+size_t svdq_fp8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+svdq_status svdq_fp8_gated_gemm(const void* act_codes, const float* act_scales, int64_t act_scale_stride,
+                                const void* gate_codes, const float* gate_scales,
+                                const void* up_codes, const float* up_scales,
+                                const void* gate_bias, const void* up_bias, int64_t M, int64_t F, int64_t K,
+                                int activation, int out_type, const float* smooth, void* out,
+                                float* out_scales, int64_t out_scale_stride,
+                                void* workspace, size_t workspace_bytes, void* stream);
+size_t svdq_fp8_gated_gemm_workspace_size(int64_t M, int64_t F, int64_t K, int out_type);
+
+/*
+ * Test hook for svdq_fp8_gemm and svdq_fp8_gated_gemm, as svdq_debug_set_w8a8_plan: tile 0
+ * chooses by shape, 1 the few-token kernel where M <= 16; 114, 213, 224, 413, 423 and 442 the
+ * tile kernel, the digits being the workgroup tile's weight rows / 64 (gated: half of them
+ * gate's, half up's), its tokens / 64 and its LDS stages (a tile of fewer than 256 weight
+ * rows cannot give coded output, which then takes a tile by shape); splits 0 by shape, else
+ * the K-splits per tile (1..16; the largest power of two up to it that the blocks of K
+ * allow).  Y may then differ in the order of its fp32 sums.  Query the workspace
+ * size after setting it.  INVALID_VALUE for other values.
+ */
+svdq_status svdq_debug_set_fp8_plan(int tile, int splits);
+
+/*
  * The norms before and after a block, fused with its gate and the residual
  * scale.  Adaptive-normalization blocks of a diffusion transformer take gate,
  * scale and shift from the modulation projections (mind-verse.de, same page and
@@ -513,7 +592,8 @@ svdq_status svdq_debug_set_w8a8_plan(int tile, int splits);
  * by it, nor by a row with infinities or NaN.  z leaves as bf16, or with
  * SVDQ_NORM_OUT_INT8 as the codes and token scales that svdq_w8a8_gemm reads:
  * those of svdq_quantize_act_int8 for v = fl32(z fl32(1/smooth)) (or z) in the
- * place of x_hat, not rounded to bf16 in between.
+ * place of x_hat, not rounded to bf16 in between; with SVDQ_NORM_OUT_FP8 likewise as
+ * those of svdq_quantize_act_fp8, which svdq_fp8_gemm and svdq_fp8_gated_gemm read.
  *
  *   x            device, bf16 or fp32 (stream_type) [M, C], rows x_stride apart
  *   y            device, bf16 [M, C], rows y_stride apart, or NULL (then no h)
@@ -526,18 +606,19 @@ svdq_status svdq_debug_set_w8a8_plan(int tile, int splits);
  *   h            device out, x's type [M, C], rows h_stride apart; may be x itself
  *                with x's stride (the stream updated in place; y, or a gate of M rows,
  *                may then be x as well, and nothing else)
- *   z            device out, bf16 [M, C] or int8 [M, C]; z_scales fp32 [M] for int8
- *   smooth       device, fp32 [C] or NULL (int8 output only)
+ *   z            device out, bf16 [M, C], int8 [M, C] or e4m3 [M, C]; z_scales fp32 [M]
+ *                for int8, fp32 [ceil(C / 128), M] for e4m3
+ *   smooth       device, fp32 [C] or NULL (8-bit output only)
  * Strides are in elements and multiples of 8 (the chunks of a modulation
  * projection's output are rows of a larger stride); strides of arrays with one
- * row are not read.  C % 8 == 0, C % 64 == 0 for int8, C <= 32768, M <= 2^24, strides <= 2^37
+ * row are not read.  C % 8 == 0, C % 64 == 0 for 8-bit output, C <= 32768, M <= 2^24, strides <= 2^37
  * (NOT_SUPPORTED beyond); M == 0 is a no-op; INVALID_VALUE for an unknown enum
  * value, a vector without the part it belongs to, a bad eps or
  * residual_scale, rows that do not divide M, and as for the other calls.
  */
 typedef enum { SVDQ_NORM_NONE = 0, SVDQ_NORM_LAYER = 1, SVDQ_NORM_RMS = 2 } svdq_norm;
 typedef enum { SVDQ_STREAM_BF16 = 0, SVDQ_STREAM_FP32 = 1 } svdq_stream_type;
-typedef enum { SVDQ_NORM_OUT_BF16 = 0, SVDQ_NORM_OUT_INT8 = 1 } svdq_norm_out;
+typedef enum { SVDQ_NORM_OUT_BF16 = 0, SVDQ_NORM_OUT_INT8 = 1, SVDQ_NORM_OUT_FP8 = 3 } svdq_norm_out;  /* 2: no type */
 svdq_status svdq_gate_norm_modulate(
     const void* x, int stream_type, int64_t x_stride, const void* y, int64_t y_stride,
     int post_norm, const void* post_weight, const void* gate, int64_t gate_rows, int64_t gate_stride,
@@ -654,6 +735,19 @@ svdq_status svdq_pack_weights_fp4(const uint16_t* w, const float* smooth, int64_
  */
 svdq_status svdq_pack_weights_int8(const uint16_t* w, const float* smooth, int64_t N, int64_t K,
                                    int8_t* w_codes, float* w_scales);
+
+/*
+ * Host packer of the 8-bit floating-point linear: W' = W diag(smooth) in double (smooth
+ * NULL: W), per 128 x 128 block (the last ones of N and K may be smaller)
+ * s = fl32(max |W'| / 448) and q = e4m3(W' / s) (nearest, ties to even, at most 448), a
+ * zero block s = 0 and codes 0.
+ *   w host bf16 [N, K]; smooth host fp32 [K] or NULL; N, K > 0
+ *   w_codes host out e4m3 [N, K]; w_scales host out fp32 [ceil(N / 128), ceil(K / 128)]
+ * A weight or product that is not finite is INVALID_VALUE.  CPU only (threads);
+ * deterministic.
+ */
+svdq_status svdq_pack_weights_fp8(const uint16_t* w, const float* smooth, int64_t N, int64_t K,
+                                  uint8_t* w_codes, float* w_scales);
 
 /*
  * Host AWQ packer (CPU, caller-owned host buffers): the offline step of the

@@ -48,6 +48,7 @@ __device__ __forceinline__ void dma4(const void* gptr, uint8_t* lds_wave_base) {
 struct TileArgs {
   Fp8Args g;
   int splits;   // over K, gridDim.y
+  int tiles;    // of the whole launch
   u32* count;   // one arrival counter per tile (splits > 1)
   float* part;  // fp32 partials [tile][splits][waves][2 H J][64][4]
 };
@@ -64,31 +65,32 @@ struct Shape {
 };
 
 enum Form { kPlain, kGated, kGatedCodes };
+// kOne: a tile per workgroup; kSplits: the same over a part of K; kMany: several tiles
+// per workgroup, one after the other, all of them whole, ceil(K / 128) % R == 0
+enum Mode { kOne, kSplits, kMany };
 
-template <int H, int J, int WN, int WM, int R, Form kForm, bool kSplit>
+template <int H, int J, int WN, int WM, int R, Form kForm, Mode kMode>
 __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_tile_kernel(const TileArgs p) {
   using Sh = Shape<H, J, WN, WM, R>;
   static_assert(R >= 2 && R <= 4, "stage buffers");
+  constexpr bool kSplit = kMode == kSplits, kWhole = kMode == kMany;
   constexpr bool kGate = kForm != kPlain;
   constexpr int kTN = Sh::kTN, kTM = Sh::kTM, kWaves = Sh::kWaves;
   constexpr int kCols = kGate ? kTN / 2 : kTN;        // output columns of a tile
   constexpr int kWaveCols = kGate ? 16 * H : 32 * H;  // and of a wave
   // one LDS object per operand (per half of the weight rows) and stage, so the compiler
   // sees that a DMA into one cannot alias reads of another
-  constexpr int kHalf = kTN / 2;
-  __shared__ __attribute__((aligned(16))) uint8_t g0[kHalf * 128], g1[kHalf * 128], u0[kHalf * 128], u1[kHalf * 128];
-  __shared__ __attribute__((aligned(16))) uint8_t g2[R > 2 ? kHalf * 128 : 16], u2[R > 2 ? kHalf * 128 : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t g3[R > 3 ? kHalf * 128 : 16], u3[R > 3 ? kHalf * 128 : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t a0[kTM * 128], a1[kTM * 128];
-  __shared__ __attribute__((aligned(16))) uint8_t a2[R > 2 ? kTM * 128 : 16], a3[R > 3 ? kTM * 128 : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t s0[kTM * 4], s1[kTM * 4], s2[R > 2 ? kTM * 4 : 16],
-      s3[R > 3 ? kTM * 4 : 16];
+#define SVDQ_STAGE(b)                                                                                            \
+  __shared__ __attribute__((aligned(16))) uint8_t g##b[R > b ? kTN * 64 : 16], u##b[R > b ? kTN * 64 : 16],      \
+      a##b[R > b ? kTM * 128 : 16], s##b[R > b ? kTM * 4 : 16];
+  SVDQ_STAGE(0) SVDQ_STAGE(1) SVDQ_STAGE(2) SVDQ_STAGE(3)
+#undef SVDQ_STAGE
+#define SVDQ_PICK(x) b == 0 ? x##0 : b == 1 ? x##1 : b == 2 ? x##2 : x##3
   // the first half of the waves' weight rows, 16 H of each wave (gated: G's), and the second
-  auto wbuf = [&](int b, int half) -> uint8_t* {
-    return half == 0 ? b == 0 ? g0 : b == 1 ? g1 : b == 2 ? g2 : g3 : b == 0 ? u0 : b == 1 ? u1 : b == 2 ? u2 : u3;
-  };
-  auto abuf = [&](int b) -> uint8_t* { return b == 0 ? a0 : b == 1 ? a1 : b == 2 ? a2 : a3; };
-  auto sbuf = [&](int b) -> uint8_t* { return b == 0 ? s0 : b == 1 ? s1 : b == 2 ? s2 : s3; };
+  auto wbuf = [&](int b, int half) -> uint8_t* { return half == 0 ? (SVDQ_PICK(g)) : (SVDQ_PICK(u)); };
+  auto abuf = [&](int b) -> uint8_t* { return SVDQ_PICK(a); };
+  auto sbuf = [&](int b) -> uint8_t* { return SVDQ_PICK(s); };
+#undef SVDQ_PICK
   __shared__ __attribute__((aligned(16))) uint8_t rows[kWaves * Sh::kTurn];  // the epilogue's own
   __shared__ float red[kForm == kGatedCodes ? kWaves * 16 * J : 1];
   __shared__ u32 arrived;
@@ -107,17 +109,10 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
   const int wm = wave % WM;
   const int l16 = lane & 15;
   const int lq = lane >> 4;
-  int tm, tn;
-  tile_of(blockIdx.x, (M + kTM - 1) / kTM, tiles_n, tm, tn);
-  const int n0 = tn * kCols, m0 = tm * kTM;
-
   // Weight scales of the wave's two halves, one of each a stage, by scalar loads (as
   // constant memory: nothing writes them during the launch) a stage ahead
   typedef const float __attribute__((address_space(4))) cfloat;
-  const int blocks_n = (N + 127) >> 7;
-  const size_t ws_at = (size_t)min((n0 + wn * kWaveCols) >> 7, blocks_n - 1) * S_all + q_begin;
-  cfloat* ws0 = (cfloat*)(p.g.w_scales + ws_at);
-  cfloat* ws1 = (cfloat*)((kGate ? p.g.up_scales : p.g.w_scales) + ws_at);
+  cfloat *ws0, *ws1;
   float sw0, sw1;
   // the half stage sums its 64 products twice (below)
   const int half_at = q_end == S_all && (K & 64) != 0 ? S - 1 : S;
@@ -126,7 +121,6 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
     sw0 = ws0[at];
     if constexpr (kGate) sw1 = ws1[at];
   };
-  load_ws(0);
 
   // DMA role: instruction k of a wave fills rows 8 (waves k + wave) + lane / 8, slot
   // lane % 8 of each row, with granule (lane % 8) ^ row[3:1].  Rows past the
@@ -140,28 +134,38 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
   static_assert(kWaves % 2 == 0 && kWd % 2 == 0 && kWd * 8 * kWaves == kTN && kAd * 8 * kWaves == kTM, "whole row runs per wave");
   static_assert(kTM % 64 == 0 && kTM <= 64 * kWaves, "the waves cover the token scales");
   const u32 wlane = (u32)(lane >> 3) * (u32)K + gran;
-  const uint8_t* abase = p.g.act + (size_t)m0 * (size_t)K;
-  const uint8_t* wbase[kWd];
-  u32 aoff[kAd];
-  // (N % 64 == 0: the 8 weight rows of an instruction are all inside or all
-  // past the end, so their address is uniform)
-#pragma unroll
-  for (int k = 0; k < kWd; ++k) {
-    const bool second = k >= kWd / 2;
-    const int row = 8 * (kWaves * (second ? k - kWd / 2 : k) + wave);  // of the half
-    if constexpr (kGate) {
-      wbase[k] = (second ? p.g.up : p.g.w) + (size_t)min(n0 + row, N - 8) * (size_t)K;
-    } else {
-      const int n = row / (16 * H) * (32 * H) + row % (16 * H) + (second ? 16 * H : 0);
-      wbase[k] = p.g.w + (size_t)min(n0 + n, N - 8) * (size_t)K;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kAd; ++k)
-    aoff[k] = (u32)(min(m0 + 8 * (kWaves * k + wave) + (lane >> 3), M - 1) - m0) * (u32)K + gran;
+  const uint8_t *abase, *sbase;
+  const uint8_t* wbase[2];  // of each half
+  u32 woff[kWd], aoff[kAd], soff;
   const int srow = 64 * (wave % (kTM / 64));  // the wave's run of token scales
-  const u32 soff = 4u * (u32)(min(m0 + srow + lane, M - 1) - m0);
-  const uint8_t* sbase = reinterpret_cast<const uint8_t*>(p.g.act_scales + m0);
+  // the tile that the DMAs fill (one or more stages ahead of the products)
+  int tn, n0, m0;
+  auto dma_tile = [&](int t) {
+    int tm;
+    tile_of(t, (M + kTM - 1) / kTM, (N + kCols - 1) / kCols, tm, tn);
+    n0 = tn * kCols, m0 = tm * kTM;
+    abase = p.g.act + (size_t)m0 * (size_t)K;
+    sbase = reinterpret_cast<const uint8_t*>(p.g.act_scales + m0);
+    // (N % 64 == 0: the 8 weight rows of an instruction are all inside or all
+    // past the end, so their address is uniform)
+    wbase[0] = p.g.w + (size_t)n0 * (size_t)K;
+    wbase[1] = kGate ? p.g.up + (size_t)n0 * (size_t)K : wbase[0];
+#pragma unroll
+    for (int k = 0; k < kWd; ++k) {
+      const bool second = k >= kWd / 2;
+      const int row = 8 * (kWaves * (second ? k - kWd / 2 : k) + wave);  // of the half
+      const int n = kGate ? row : row / (16 * H) * (32 * H) + row % (16 * H) + (second ? 16 * H : 0);
+      woff[k] = (u32)(kWhole ? n : min(n0 + n, N - 8) - n0) * (u32)K;
+    }
+  };
+  auto lane_offsets = [&] {
+#pragma unroll
+    for (int k = 0; k < kAd; ++k) {
+      const int row = 8 * (kWaves * k + wave) + (lane >> 3);
+      aoff[k] = (u32)(kWhole ? row : min(m0 + row, M - 1) - m0) * (u32)K + gran;
+    }
+    soff = 4u * (u32)(kWhole ? srow + lane : min(m0 + srow + lane, M - 1) - m0);
+  };
   struct Col {
     u32 x, back;
     const uint8_t* s;
@@ -174,12 +178,12 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
   // DMA k of a stage: the first half of the weights, tokens, token scales, the second half
   auto dma_one = [&](int k, const Col& col, auto bc) {
     constexpr int b = decltype(bc)::value, h = kWd / 2;
-    if (k < h) dma16(wbase[k] + col.x + (wlane - col.back), wbuf(b, 0) + 1024 * (kWaves * k + wave));
+    if (k < h) dma16(wbase[0] + (woff[k] + col.x) + (wlane - col.back), wbuf(b, 0) + 1024 * (kWaves * k + wave));
     else if (k < h + kAd)
       dma16(abase + col.x + (aoff[k - h] - col.back), abuf(b) + 1024 * (kWaves * (k - h) + wave));
     else if (k == h + kAd) dma4(col.s + soff, sbuf(b) + 4 * srow);
     else
-      dma16(wbase[k - kAd - 1] + col.x + (wlane - col.back), wbuf(b, 1) + 1024 * (kWaves * (k - h - kAd - 1) + wave));
+      dma16(wbase[1] + (woff[k - kAd - 1] + col.x) + (wlane - col.back), wbuf(b, 1) + 1024 * (kWaves * (k - h - kAd - 1) + wave));
   };
   // With two stages of four phases (kTwice) a stage's LDS is given back in two parts: its
   // tokens and the first half of its weights have been read when its second phase begins,
@@ -194,12 +198,15 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
   };
 
   // Fragments: lane (l16, lq) takes granules lq and lq + 4 of row 16 i + l16.
-  constexpr int kG = H > 1 ? 2 : 1;       // weight tiles of a phase
+  // The smaller tiles of an even number of stages take a whole stage's fragments a stage
+  // ahead of its MFMAs (kAhead), so that one phase and one trip to LDS remain per stage.
+  constexpr bool kAhead = H <= 2 && R % 2 == 0;
+  constexpr int kG = kAhead ? 2 * H : H > 1 ? 2 : 1;  // weight tiles of a phase
   constexpr int kP = 2 * H / kG;          // phases of a stage; the first half of them is the first half of the rows
   constexpr int kSlots = kG * J;          // MFMAs of a phase
   const int fo = 128 * l16 + 16 * (lq ^ (l16 >> 1));
   const int wrow = wn * 16 * H * 128, arow = wm * 16 * J * 128;
-  v8i fw[2][kG], fa[J];
+  v8i fw[2][kG], fa[kAhead ? 2 : 1][J];
   float st[J];
   // (the address anew for each phase: registers for every buffer's are worth more)
   auto at_row = [&] {
@@ -220,22 +227,16 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
   };
 
   v4f acc[2 * H][J];
-#pragma unroll
-  for (int i = 0; i < 2 * H; ++i)
-#pragma unroll
-    for (int j = 0; j < J; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
   // MFMA results join their sums kLag slots later
   constexpr int kLag = kSlots >= 4 ? 4 : 2;
+  constexpr int kScales = kAhead && kGate ? 2 : 1;
   v4f pend[kLag];
-#pragma unroll
-  for (int t = 0; t < kLag; ++t) pend[t] = v4f{0.f, 0.f, 0.f, 0.f};
-  float c[J];  // the token tiles' scales for the products of a phase
-#pragma unroll
-  for (int j = 0; j < J; ++j) c[j] = 0.f;
+  float c[kScales][J];  // the token tiles' scales for the products of a phase (of each half)
   auto join = [&](int ph, int t) {  // the results of slot t of phase ph
     v4f& s = acc[kG * ph + t % kG][t / kG];
+    const float f = c[kScales == 2 ? t % kG / H : 0][t / kG];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] = __builtin_fmaf(pend[t % kLag][e], c[t / kG], s[e]);
+    for (int e = 0; e < 4; ++e) s[e] = __builtin_fmaf(pend[t % kLag][e], f, s[e]);
   };
   // slot t of phase ph: the MFMA of weight tile t % kG and token tile t / kG; the results of
   // the MFMA kLag slots before it are added
@@ -253,10 +254,11 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
   using B1 = std::integral_constant<int, 1>;
   using B2 = std::integral_constant<int, 2>;
   using B3 = std::integral_constant<int, 3>;
+  int shift = 0;  // stages by which the DMAs run ahead into the next tile
   // stage q from buffer bc: its tokens, its token scales and the first phase's weights
   // are in registers
   auto iteration = [&](int q, auto bc) {
-    constexpr int b = decltype(bc)::value;
+    constexpr int b = decltype(bc)::value, set = kAhead ? b & 1 : 0;
     using BC = std::integral_constant<int, b>;
     using BN = std::integral_constant<int, (b + 1) % R>;
     const float half = q == half_at ? 0.5f : 1.0f, up = kGate ? half * sw1 : 0.f;
@@ -266,7 +268,7 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
     for (int ph = 0; ph < kP; ++ph) {
       if (ph == kP - 2) load_ws(q + 1);
       const bool last = ph == kP - 1, part = kTwice && ph == 1, after = kTwice && ph == 2;
-      const Col col = stage_col(q + R);
+      const Col col = stage_col(q + R + shift);
       const int at = at_row();
       if (last || part) {
         __builtin_amdgcn_sched_barrier(0);
@@ -275,14 +277,18 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
         wait_vm_lds<kTwice ? kDmas : (R - 2) * kDmas>();
         barrier();
       }
-      static_assert(kP % 2 == 0, "the next stage's first phase takes the other weight registers");
+      static_assert(kAhead || kP % 2 == 0, "the next stage's first phase takes the other weight registers");
+      if (kAhead) load_ws(q + 1);
 #pragma unroll
       for (int t = 0; t < kSlots; ++t) {
         __builtin_amdgcn_sched_barrier(0);
-        slot(ph, t, fw[ph & 1][t % kG], fa[t / kG]);
+        slot(ph, t, fw[kAhead ? set : ph & 1][t % kG], fa[set][t / kG]);
         // (a token tile's scale is needed kLag slots after its first MFMA, and was kLag
         // slots after its last one)
-        if ((ph == 0 || (kGate && ph == kP / 2)) && t % kG == kG - 1) c[t / kG] = st[t / kG] * (ph == 0 ? sw : up);
+        if ((ph == 0 || (kGate && ph == kP / 2)) && t % kG == kG - 1) {
+          c[0][t / kG] = st[t / kG] * (ph == 0 ? sw : up);
+          if constexpr (kScales == 2) c[1][t / kG] = st[t / kG] * up;
+        }
         if (!last) {
           if (t < kG) fw[(ph + 1) & 1][t] = read_w(BC{}, kG * (ph + 1) + t, at);
         } else {
@@ -290,8 +296,17 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
 #pragma unroll
             for (int j = 0; j < J; ++j) next[j] = read_s(BN{}, j);
           }
-          if (t < kG) fw[0][t] = read_w(BN{}, t, at);
-          if (t % kG == kG - 1) fa[t / kG] = read_a(BN{}, t / kG, at);
+          if constexpr (kAhead) {
+            constexpr int kEach = (2 * H + J + kSlots - 1) / kSlots;  // fragments
+#pragma unroll
+            for (int f = kEach * t; f < kEach * (t + 1) && f < 2 * H + J; ++f) {
+              if (f < J) fa[set ^ 1][f] = read_a(BN{}, f, at);
+              else fw[set ^ 1][f - J] = read_w(BN{}, f - J, at);
+            }
+          } else {
+            if (t < kG) fw[0][t] = read_w(BN{}, t, at);
+            if (t % kG == kG - 1) fa[0][t / kG] = read_a(BN{}, t / kG, at);
+          }
         }
         if (last || part || after) {  // the early DMAs are spread over two phases
           const int mid = (kEarly + 1) / 2;
@@ -306,32 +321,58 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
 #pragma unroll
     for (int j = 0; j < J; ++j) st[j] = next[j];
   };
+  int tile = blockIdx.x;
+  dma_tile(tile);
+  lane_offsets();
   dma_stage(0, B0{});
   dma_stage(1, B1{});
   if constexpr (R > 2) dma_stage(2, B2{});
   if constexpr (R > 3) dma_stage(3, B3{});
   wait_vm_lds<(R - 1) * kDmas + kLate>();
   barrier();
+  for (;;) {
+  const int tn0 = tn, nt = n0, mt = m0;  // of the products
+  const size_t ws_at = (size_t)min((nt + wn * kWaveCols) >> 7, ((N + 127) >> 7) - 1) * S_all + q_begin;
+  ws0 = (cfloat*)(p.g.w_scales + ws_at);
+  ws1 = (cfloat*)((kGate ? p.g.up_scales : p.g.w_scales) + ws_at);
+  load_ws(0);
 #pragma unroll
   for (int t = 0; t < kG; ++t) fw[0][t] = read_w(B0{}, t, fo);
 #pragma unroll
-  for (int j = 0; j < J; ++j) fa[j] = read_a(B0{}, j, fo), st[j] = read_s(B0{}, j);
-
+  for (int j = 0; j < J; ++j) fa[0][j] = read_a(B0{}, j, fo), st[j] = read_s(B0{}, j);
+#pragma unroll
+  for (int i = 0; i < 2 * H; ++i)
+#pragma unroll
+    for (int j = 0; j < J; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < kLag; ++t) pend[t] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < J; ++j) c[0][j] = c[kScales - 1][j] = 0.f;
+  const int next = tile + (int)gridDim.x;
+  const bool more = kWhole && next < p.tiles;
+  shift = 0;
   int q = 0;
   for (; q + R <= S; q += R) {
+    // the last R stages fetch the first of the next tile
+    if (more && q + R == S) {
+      dma_tile(next);
+      shift = -S;
+    }
     iteration(q, B0{});
     iteration(q + 1, B1{});
     if constexpr (R > 2) iteration(q + 2, B2{});
     if constexpr (R > 3) iteration(q + 3, B3{});
   }
-  if (q < S) iteration(q, B0{});
-  if constexpr (R > 2)
-    if (q + 1 < S) iteration(q + 1, B1{});
-  if constexpr (R > 3)
-    if (q + 2 < S) iteration(q + 2, B2{});
+  if constexpr (!kWhole) {
+    if (q < S) iteration(q, B0{});
+    if constexpr (R > 2)
+      if (q + 1 < S) iteration(q + 1, B1{});
+    if constexpr (R > 3)
+      if (q + 2 < S) iteration(q + 2, B2{});
+  }
 #pragma unroll
   for (int t = 0; t < kLag; ++t) join(kP - 1, kSlots + t - kLag);
-  wait_vm_lds<0>();  // no DMA may land in the LDS that the epilogue or a next workgroup takes
+  if constexpr (!kWhole) wait_vm_lds<0>();  // no DMA may land in a next workgroup's LDS
 
   if constexpr (kSplit) {
     // Every workgroup stores its fp32 sums with agent-coherent stores, waits for them and
@@ -377,7 +418,7 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
   __asm__ volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(el));
   const int e16 = el & 15, eq = el >> 4;
   uint8_t* turn = rows + wave * Sh::kTurn;
-  const int nw = n0 + wn * kWaveCols, mw = m0 + wm * 16 * J;  // the wave's first column and row
+  const int nw = nt + wn * kWaveCols, mw = mt + wm * 16 * J;  // the wave's first column and row
   auto bias4 = [&](const uint16_t* b, int n, float (&f)[4]) {
     const uint2 v = b != nullptr ? *reinterpret_cast<const uint2*>(b + min(n, N - 4)) : uint2{0u, 0u};
     f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
@@ -413,7 +454,7 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
     // a token's block of 128 features lies in the WN waves of a tile row: their
     // maxima meet in LDS.  Features past the end (a half last block) are whole waves'
     static_assert(kCols == 128, "a tile holds a block of features");
-    const bool in = nw < N;
+    const bool in = kWhole || nw < N;
     if (p.g.smooth != nullptr) {
 #pragma unroll
       for (int i = 0; i < H; ++i) {
@@ -435,8 +476,9 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
       m = max_rows4(in ? m : 0.f);
       if (eq == 0) red[(wn * WM + wm) * 16 * J + 16 * j + e16] = m;
     }
-    __syncthreads();
-    if (!in) return;
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this wave's maxima are in LDS
+    barrier();
+    if (!in) return;  // (of the one tile: whole ones have all features)
     constexpr int kRow = 16 * H;  // bytes of a row of the wave's codes
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -446,7 +488,7 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
       float s, inv;
       block_scale(m, s, inv);
       const int tok = mw + 16 * j + e16;
-      if (wn == 0 && eq == 0 && tok < M) p.g.out_scales[(size_t)tn * p.g.out_stride + tok] = s;
+      if (wn == 0 && eq == 0 && tok < M) p.g.out_scales[(size_t)tn0 * p.g.out_stride + tok] = s;
 #pragma unroll
       for (int i = 0; i < H; ++i) {
         const float v[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
@@ -494,6 +536,10 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
         __asm__ volatile("" ::: "memory");  // (a wave's LDS operations run in order)
       }
   }
+  if (!more) break;
+  tile = next;
+  }
+  if constexpr (kWhole) wait_vm_lds<0>();  // no DMA may land in a next workgroup's LDS
 }
 
 struct Plan {
@@ -506,14 +552,16 @@ struct Plan {
 // Workgroup tiles, the test hook's name of each (weight rows / 64, tokens / 64, LDS stages)
 // and what a launch takes by the model of w8a8_gemm.hip: base + n (fill + S step) us with n
 // workgroups on the busiest compute unit and S stages of 128 k, pairs of workgroups at fill2
-// and step2 where two share a compute unit.
+// and step2 where two share a compute unit.  Fitted to 634 shapes (17 to 4608 tokens, K 512
+// to 10240, 384 to 12288 rows, 40 % of them gated), every tile and split timed with weights
+// from HBM: the plan's pick is within 0.5 % (geometric mean) of the best measured one, 25 % at most.
 #define SVDQ_SHAPES(X)                                   \
-  X(442, 4, 4, 2, 4, 2, -3.29, 11.18, 1.25, 0.0, 0.0)    \
-  X(423, 2, 4, 4, 2, 3, -1.0, 8.0, 0.70, 0.0, 0.0)       \
-  X(413, 2, 2, 4, 2, 3, 1.0, 5.0, 0.45, 0.0, 0.0)        \
-  X(224, 2, 2, 2, 4, 4, 1.06, 4.89, 0.45, 0.0, 0.0)      \
-  X(213, 2, 2, 2, 2, 3, 2.0, 2.83, 0.26, 3.5, 0.45)      \
-  X(114, 1, 2, 2, 2, 4, 3.00, 1.45, 0.18, 2.07, 0.365)
+  X(442, 4, 4, 2, 4, 2, -6.73, 14.87, 1.333, 0.0, 0.0)   \
+  X(423, 2, 4, 4, 2, 3, -0.81, 6.62, 0.872, 0.0, 0.0)    \
+  X(413, 2, 2, 4, 2, 3, 0.85, 3.58, 0.639, 0.0, 0.0)     \
+  X(224, 2, 2, 2, 4, 4, 0.51, 4.09, 0.525, 0.0, 0.0)     \
+  X(213, 2, 2, 2, 2, 3, 3.03, 0.64, 0.381, 2.16, 0.717)  \
+  X(114, 1, 2, 2, 2, 4, 2.74, 0.86, 0.249, 1.52, 0.490)
 struct ShapeInfo {
   int code, tn, tm, waves, wgs;
   double base, fill, step, fill2, step2;
@@ -563,8 +611,50 @@ Plan plan_of(const Fp8Args& a) {
       } else {
         cost += n * (s.fill + S * s.step);
       }
-      if (splits > 1) cost += 2.54 + 0.52 * splits + 0.57 * (s.tn / 64) * (s.tm / 64);  // the partials' round trips
+      if (splits > 1) cost += -0.44 + 0.66 * splits + 0.89 * (s.tn / 64) * (s.tm / 64);  // the partials' round trips
       if (best.shape < 0 || cost < best.cost || (forced > 0 && best.shape == i)) best = Plan{i, (int)tiles, splits, cost};
+    }
+  }
+  return best;
+}
+
+// The launches of a product: the tokens [0, m1) in whole rounds of one of the largest
+// tiles, and the rest on the tile that suits it (m1 = M: one launch).  The last round of a
+// large tile otherwise leaves most compute units idle.
+// kSecondLaunch: what a second launch takes beyond the model's sum, in us.
+constexpr double kSecondLaunch = 6.5;
+struct Launches {
+  int64_t m1;
+  Plan first, rest;
+};
+Fp8Args part_of(const Fp8Args& a, int64_t m0, int64_t m1) {
+  Fp8Args part = a;
+  part.M = (int)(m1 - m0);
+  part.act += (size_t)m0 * (size_t)a.K;
+  part.act_scales += m0;
+  part.out = static_cast<uint8_t*>(a.out) + (size_t)m0 * (size_t)a.N * (a.out_scales != nullptr ? 1 : 2);
+  if (a.out_scales != nullptr) part.out_scales += m0;
+  return part;
+}
+Launches launches_of(const Fp8Args& a) {
+  Launches best{a.M, plan_of(a), Plan{}};
+  if (g_tile.load(std::memory_order_relaxed) > 1 || g_splits.load(std::memory_order_relaxed) > 0) return best;
+  const int cus = current_cus();
+  const double S = (double)((a.K + 127) / 128);
+  double best_cost = best.first.cost;
+  for (int i = 0; i < 2; ++i) {
+    const ShapeInfo& s = kShapes[i];
+    const int64_t cols = a.up != nullptr ? s.tn / 2 : s.tn;
+    const int64_t nt = (a.N + cols - 1) / cols, mt = (a.M + s.tm - 1) / s.tm;
+    const int64_t rounds = nt * mt / cus, mt1 = rounds * cus / nt;
+    if (mt1 <= 0 || mt1 * s.tm >= a.M || mt1 * nt * s.waves * 64 >= (1ll << 32)) continue;
+    Fp8Args rest = a;
+    rest.M = (int)(a.M - mt1 * s.tm);
+    Launches l{mt1 * s.tm, Plan{i, (int)(mt1 * nt), 1, 0.0}, plan_of(rest)};
+    l.first.cost = kSecondLaunch + s.base + (double)((mt1 * nt + cus - 1) / cus) * (s.fill + S * s.step);
+    if (l.first.cost + l.rest.cost < best_cost) {
+      best = l;
+      best_cost = l.first.cost + l.rest.cost;
     }
   }
   return best;
@@ -574,10 +664,21 @@ template <int H, int J, int WN, int WM, int R, Form kForm>
 void tile_form(const TileArgs& t, int tiles, hipStream_t stream) {
   using Sh = Shape<H, J, WN, WM, R>;
   const dim3 block(Sh::kThreads);
+  // whole tiles, more than the chip holds at once, and no long K: one workgroup per compute
+  // unit (of the largest tile, which the plan takes for such products).  Four rounds of
+  // 256 x 256: K 2304 153.6 -> 149.5 us, 3072 187.2 -> 185.6, 8192 446.5 -> 450.7
+  if constexpr (H == 4) {
+    const int cus = current_cus();
+    if (t.splits == 1 && tiles > cus && t.g.M % Sh::kTM == 0 && t.g.N % (kForm == kPlain ? Sh::kTN : Sh::kTN / 2) == 0 &&
+        (t.g.K + 127) / 128 % R == 0 && t.g.K <= 4096) {
+      hipLaunchKernelGGL((fp8_tile_kernel<H, J, WN, WM, R, kForm, kMany>), dim3(cus), block, 0, stream, t);
+      return;
+    }
+  }
   if (t.splits > 1)
-    hipLaunchKernelGGL((fp8_tile_kernel<H, J, WN, WM, R, kForm, true>), dim3(tiles, t.splits), block, 0, stream, t);
+    hipLaunchKernelGGL((fp8_tile_kernel<H, J, WN, WM, R, kForm, kSplits>), dim3(tiles, t.splits), block, 0, stream, t);
   else
-    hipLaunchKernelGGL((fp8_tile_kernel<H, J, WN, WM, R, kForm, false>), dim3(tiles), block, 0, stream, t);
+    hipLaunchKernelGGL((fp8_tile_kernel<H, J, WN, WM, R, kForm, kOne>), dim3(tiles), block, 0, stream, t);
 }
 
 template <int H, int J, int WN, int WM, int R>
@@ -620,14 +721,14 @@ void set_fp8_plan_override(int tile, int splits) {
 }
 
 size_t fp8_workspace_bytes(const Fp8Args& a) {
-  return few_tokens(a) ? fp8_skinny_workspace_bytes(a) : plan_bytes(plan_of(a));
+  if (few_tokens(a)) return fp8_skinny_workspace_bytes(a);
+  const Launches l = launches_of(a);
+  return std::max(plan_bytes(l.first), l.m1 < a.M ? plan_bytes(l.rest) : 0);
 }
 
-hipError_t launch_fp8_gemm(const Fp8Args& a, Workspace ws, hipStream_t stream) {
-  if (few_tokens(a)) return launch_fp8_skinny(a, ws, stream);
-  const Plan p = plan_of(a);
+static hipError_t launch_plan(const Fp8Args& a, const Plan& p, const Workspace& ws, hipStream_t stream) {
   if (p.shape < 0 || plan_bytes(p) > ws.bytes) return hipErrorInvalidValue;
-  TileArgs t{a, p.splits, nullptr, nullptr};
+  TileArgs t{a, p.splits, p.tiles, nullptr, nullptr};
   if (p.splits > 1) {
     t.count = ws_counters(ws);
     t.part = static_cast<float*>(ws_scratch(ws));
@@ -639,6 +740,14 @@ hipError_t launch_fp8_gemm(const Fp8Args& a, Workspace ws, hipStream_t stream) {
 #undef SVDQ_GO
     default: return hipErrorInvalidValue;
   }
+}
+
+hipError_t launch_fp8_gemm(const Fp8Args& a, Workspace ws, hipStream_t stream) {
+  if (few_tokens(a)) return launch_fp8_skinny(a, ws, stream);
+  const Launches l = launches_of(a);
+  const hipError_t e = launch_plan(part_of(a, 0, l.m1), l.first, ws, stream);
+  if (e != hipSuccess || l.m1 == a.M) return e;
+  return launch_plan(part_of(a, l.m1, a.M), l.rest, ws, stream);
 }
 
 }  // namespace svdq

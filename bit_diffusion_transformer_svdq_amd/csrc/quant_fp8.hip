@@ -87,20 +87,23 @@ hipError_t go(const QuantFp8Args& a, hipStream_t stream) {
 
 }  // namespace
 
-// M <= 2^24 and K <= 65536: with 16 rows a wave, 2^20 runs of 128 column groups are 2^27
-// waves of 64 lanes, past the launch limit of 2^32 threads; the launcher cuts such
-// calls into parts of whole runs
+// Rows per wave: one while a compute unit has no more than 64 waves of one row, else four
+// (us, x from HBM, 1 / 2 / 4 / 8 / 16 rows: 512 x 3840 3.5 / 3.9 / 4.2 / 5.2 / 7.4; 1333 x 1920 3.9 / 4.4 /
+// 4.8 / 5.3 / 7.6, smoothed 4.8 / 4.9 / 5.6 / 6.2 / 8.8; 4608 x 3072 11.2 / 11.6 / 10.4 / 11.4 / 12.8, smoothed
+// 13.7 / 12.8 / 11.9 / 13.2 / 14.7: 4.1 TB/s, 3.6 smoothed).
+// 2^24 rows of 65536 channels would be 2^29 waves, past the launch limit of 2^32
+// threads: such calls are cut into parts of whole runs.
 hipError_t launch_quant_fp8(const QuantFp8Args& args, hipStream_t stream) {
   QuantFp8Args a = args;
   const int64_t col_groups = (a.K + 511) / 512;
-  const int64_t most = ((1ll << 25) / col_groups) * 16;  // rows whose waves stay below 2^25
+  const bool one = args.M * col_groups <= 64 * (int64_t)current_cus();
+  const int64_t most = ((1ll << 25) / col_groups) * 4;  // rows whose waves stay below 2^25
   for (int64_t m = 0; m < args.M; m += most) {
     a.M = (int)std::min<int64_t>(most, args.M - m);
     a.x = args.x + (size_t)m * args.K;
     a.codes = args.codes + (size_t)m * args.K;
     a.scales = args.scales + m;
-    const int64_t waves1 = (int64_t)a.M * col_groups, cus = current_cus();
-    const hipError_t e = waves1 <= 8 * cus ? go<1>(a, stream) : waves1 <= 64 * cus ? go<4>(a, stream) : go<16>(a, stream);
+    const hipError_t e = one ? go<1>(a, stream) : go<4>(a, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

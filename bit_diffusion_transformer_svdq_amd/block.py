@@ -20,6 +20,7 @@ import ctypes
 import numpy as np
 import torch
 
+from . import _WS, _workspace
 from ._lib import check, lib
 
 _NORMS = {"none": 0, "layer": 1, "rms": 2}
@@ -97,15 +98,20 @@ def _gemm_workspace(need, device, stream, given):
     """As the other calls' workspaces, except under capture: there every call gets
     memory of the graph's own, its arrival counters cleared by the graph, so that
     graphs captured on one stream share nothing."""
-    from . import _workspace
-    if given is None and stream is not None:
+    if given is not None:
+        return _workspace(need, device, stream, given)
+    if stream is not None:
         with torch.cuda.stream(stream):
             return _gemm_workspace(need, device, None, None)
-    if given is None and torch.cuda.is_current_stream_capturing():
+    if torch.cuda.is_current_stream_capturing():
         ws = torch.empty((need,), dtype=torch.uint8, device=device)
         ws[:_WS_COUNTERS].zero_()
         return ws.data_ptr(), need
-    return _workspace(need, device, stream, given)
+    # (the current stream's, if it is large enough, without a Stream object: 2.5 us less per call)
+    buf = _WS.get((device.index, _raw_current(device.index)))
+    if buf is not None and buf.numel() >= need:
+        return buf.data_ptr(), buf.numel()
+    return _workspace(need, device, None, None)
 
 
 def _refuse(t, dtype, shape, idx, name):

@@ -276,6 +276,9 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
         // those issued after these may still be in flight
         wait_vm_lds<kTwice ? kDmas : (R - 2) * kDmas>();
         barrier();
+        // (the last phase, which fetches what the next stage begins with, goes ahead of the
+        // SIMD's other wave: 4096 x 8192 -> 4096 116 -> 115 us)
+        if (kTwice && last) __builtin_amdgcn_s_setprio(1);
       }
       static_assert(kAhead || kP % 2 == 0, "the next stage's first phase takes the other weight registers");
       if (kAhead) load_ws(q + 1);
@@ -318,6 +321,7 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
       }
     }
     __builtin_amdgcn_sched_barrier(0);
+    if (kTwice) __builtin_amdgcn_s_setprio(0);
 #pragma unroll
     for (int j = 0; j < J; ++j) st[j] = next[j];
   };
@@ -694,10 +698,19 @@ hipError_t tile_go(const TileArgs& t, int tiles, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The weight-streaming kernel for up to 16 tokens
+// The weight-streaming kernel for up to 16 tokens, but for long K (up to 4 tokens, and
+// gated not at all) and many rows (up to 4 tokens); always into codes.  Measured, it against
+// the best tile, weights from HBM, us, 1 / 16 tokens: 3072 -> 3072 4.2 / 5.2 against 7.9 / 8.1;
+// 3072 -> 12288 10.2 / 12.9 against 12.7 / 13.0; 12288 -> 3072 13.1 / 16.1 against 13.6 / 13.8; gated 3072 ->
+// 3072 6.6 / 8.0 against 8.8 / 9.0, 2304 -> 6144 8.6 / 10.4 against 9.0 / 9.0, 8192 -> 1024 11.6 / 14.6
+// against 10.2 / 10.3; into codes 3072 -> 3072 8.6 / 10.0 against 14.1 / 14.4.
 bool few_tokens(const Fp8Args& a) {
   const int t = g_tile.load(std::memory_order_relaxed);
-  return t <= 1 && a.M <= 16;
+  if (t > 1 || a.M > 16) return false;
+  if (t == 1 || a.out_scales != nullptr) return true;
+  const bool gated = a.up != nullptr;
+  if (a.K > 4096) return !gated && a.M <= 4;
+  return a.M <= 4 || (gated ? 2 : 1) * (int64_t)a.N <= 8192;
 }
 
 size_t plan_bytes(const Plan& p) {

@@ -3,7 +3,7 @@
 //
 // With few tokens the product is bound by reading the weights once (N K bytes, twice
 // that gated).  A workgroup owns 16 weight rows (gated: 16 rows of each projection) and
-// its 8 waves divide the blocks of K: each wave reads its part of the rows straight into
+// its 4 or 8 waves divide the blocks of K: each wave reads its part of the rows straight into
 // registers (16 rows x 128 bytes, the K of one v_mfma_f32_16x16x128_f8f6f4, in two load
 // instructions), the same part of the token rows from L2, and adds each block's product to
 // fp32 sums with the block's scale.  The waves' sums are added in LDS in wave order.
@@ -24,8 +24,6 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 8;
-constexpr int kThreads = 64 * kWaves;
 constexpr int kBatch = 2;  // blocks loaded together
 constexpr int kMaxTokens = 16;
 
@@ -35,8 +33,8 @@ struct SkinnyArgs {
   float* h;        // fp32 [N / 16][16 tokens][16 features]
 };
 
-template <bool kGate, bool kCodes>
-__global__ __launch_bounds__(kThreads) void fp8_skinny_kernel(const SkinnyArgs p) {
+template <int kWaves, bool kGate, bool kCodes>
+__global__ __launch_bounds__(64 * kWaves) void fp8_skinny_kernel(const SkinnyArgs p) {
   constexpr int kProj = kGate ? 2 : 1;
   __shared__ __attribute__((aligned(16))) v4f red[kWaves][kProj][64];
   __shared__ row_u32 arrived;
@@ -203,6 +201,12 @@ __global__ __launch_bounds__(kThreads) void fp8_skinny_kernel(const SkinnyArgs p
 
 }  // namespace
 
+// Waves per workgroup: four up to 16 blocks of K (each wave then has a batch or two) and
+// into codes, else eight.  Measured, one token, weights from HBM, 4 / 8 waves, us: K 1024 -> 9216 4.2 / 5.9,
+// gated 6.7 / 9.8, into codes 8.8 / 12.3; 1536 -> 1536 3.2 / 3.6, 4.1 / 4.8, 6.2 / 6.9; 2304 -> 6144 6.2 /
+// 5.7, 9.9 / 9.3, 11.4 / 11.0; 3072 -> 12288 11.1 / 10.2, 17.6 / 17.7, 19.3 / 22.1; 12288 -> 3072 15.4 / 13.4,
+// 20.8 / 21.5, 22.2 / 22.6.  (16 waves, and batches of one and four blocks, were no better: 3072 -> 12288
+// 13.6, 10.5, 11.9.)  10.2 us is 3.7 TB/s over the weights, launch included.
 size_t fp8_skinny_workspace_bytes(const Fp8Args& a) {
   if (a.out_scales == nullptr) return 0;
   return ws_bytes((size_t)(a.N + 127) / 128, (size_t)a.N * kMaxTokens * sizeof(float));
@@ -211,15 +215,18 @@ size_t fp8_skinny_workspace_bytes(const Fp8Args& a) {
 hipError_t launch_fp8_skinny(const Fp8Args& a, Workspace ws, hipStream_t stream) {
   if (a.M > kMaxTokens || fp8_skinny_workspace_bytes(a) > ws.bytes) return hipErrorInvalidValue;
   SkinnyArgs p{a, nullptr, nullptr};
-  const dim3 grid(a.N / 16), block(kThreads);
+  const dim3 grid(a.N / 16);
+  const bool four = a.K <= 2048;
   if (a.up == nullptr) {
-    hipLaunchKernelGGL((fp8_skinny_kernel<false, false>), grid, block, 0, stream, p);
+    if (four) hipLaunchKernelGGL((fp8_skinny_kernel<4, false, false>), grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL((fp8_skinny_kernel<8, false, false>), grid, dim3(512), 0, stream, p);
   } else if (a.out_scales == nullptr) {
-    hipLaunchKernelGGL((fp8_skinny_kernel<true, false>), grid, block, 0, stream, p);
+    if (four) hipLaunchKernelGGL((fp8_skinny_kernel<4, true, false>), grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL((fp8_skinny_kernel<8, true, false>), grid, dim3(512), 0, stream, p);
   } else {
     p.count = ws_counters(ws);
     p.h = static_cast<float*>(ws_scratch(ws));
-    hipLaunchKernelGGL((fp8_skinny_kernel<true, true>), grid, block, 0, stream, p);
+    hipLaunchKernelGGL((fp8_skinny_kernel<4, true, true>), grid, dim3(256), 0, stream, p);
   }
   return hipGetLastError();
 }

@@ -38,6 +38,9 @@ Rows scale_rows(const float* p, int64_t stride, int64_t M, int64_t width, const 
   return Rows{p, one ? 0 : sz(stride, 4), sz(M, 4), (size_t)blocks(width), name};
 }
 
+// the scales of a run of tokens may start at any of them
+bool bad_scales(const float* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
 Rows flat(const void* p, size_t bytes, const char* name) { return Rows{p, 0, bytes, 1, name}; }
 
 svdq::Fp8Args sizes(int64_t M, int64_t N, int64_t K, bool gated, bool coded) {
@@ -54,10 +57,12 @@ svdq::Fp8Args sizes(int64_t M, int64_t N, int64_t K, bool gated, bool coded) {
 svdq_status run(const svdq::Fp8Args& a, void* workspace, size_t workspace_bytes, size_t need, const char* query,
                 void* stream, const char* what) {
   const bool gated = a.up != nullptr, coded = a.out_scales != nullptr;
-  for (const void* p : {(const void*)a.act, (const void*)a.act_scales, (const void*)a.w, (const void*)a.w_scales,
-                        (const void*)a.up, (const void*)a.up_scales, (const void*)a.bias, (const void*)a.up_bias,
-                        (const void*)a.smooth, (const void*)a.out, (const void*)a.out_scales})
+  for (const void* p : {(const void*)a.act, (const void*)a.w, (const void*)a.w_scales, (const void*)a.up,
+                        (const void*)a.up_scales, (const void*)a.bias, (const void*)a.up_bias, (const void*)a.smooth,
+                        (const void*)a.out})
     if (bad_ptr(p)) return fail(SVDQ_STATUS_INVALID_VALUE, "device pointers must be 16-byte aligned");
+  if (bad_scales(a.act_scales) || bad_scales(a.out_scales))
+    return fail(SVDQ_STATUS_INVALID_VALUE, "token scales must be 4-byte aligned");
   svdq_status s = check_workspace(workspace, workspace_bytes, need, query);
   if (s != SVDQ_STATUS_SUCCESS) return s;
   const size_t wb = sz(a.N, a.K), sb = sz(blocks(a.N), blocks(a.K), 4);
@@ -93,8 +98,9 @@ svdq_status svdq_quantize_act_fp8(const void* x, const float* smooth, int64_t M,
   if (!x || !act_codes || !act_scales) return fail(SVDQ_STATUS_INVALID_VALUE, "null x/act_codes/act_scales");
   s = check_stride(act_scale_stride, M, K, "act_scales");
   if (s != SVDQ_STATUS_SUCCESS) return s;
-  if (bad_ptr(x) || bad_ptr(smooth) || bad_ptr(act_codes) || bad_ptr(act_scales))
+  if (bad_ptr(x) || bad_ptr(smooth) || bad_ptr(act_codes))
     return fail(SVDQ_STATUS_INVALID_VALUE, "device pointers must be 16-byte aligned");
+  if (bad_scales(act_scales)) return fail(SVDQ_STATUS_INVALID_VALUE, "token scales must be 4-byte aligned");
   const Rows codes = flat(act_codes, sz(M, K), "act_codes"),
              scales = scale_rows(act_scales, act_scale_stride, M, K, "act_scales"), rx = flat(x, sz(M, K, 2), "x"),
              sm = flat(smooth, sz(K, 4), "smooth");

@@ -228,7 +228,7 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
 
   v4f acc[2 * H][J];
   // MFMA results join their sums kLag slots later
-  constexpr int kLag = kSlots >= 4 ? 4 : 2;
+  constexpr int kLag = kSlots % 4 == 0 ? 4 : kSlots % 3 == 0 ? 3 : 2;
   constexpr int kScales = kAhead && kGate ? 2 : 1;
   v4f pend[kLag];
   float c[kScales][J];  // the token tiles' scales for the products of a phase (of each half)
@@ -556,16 +556,17 @@ struct Plan {
 // Workgroup tiles, the test hook's name of each (weight rows / 64, tokens / 64, LDS stages)
 // and what a launch takes by the model of w8a8_gemm.hip: base + n (fill + S step) us with n
 // workgroups on the busiest compute unit and S stages of 128 k, pairs of workgroups at fill2
-// and step2 where two share a compute unit.  Fitted to 634 shapes (17 to 4608 tokens, K 512
+// and step2 where two share a compute unit.  Fitted to 554 shapes (17 to 4608 tokens, K 512
 // to 10240, 384 to 12288 rows, 40 % of them gated), every tile and split timed with weights
-// from HBM: the plan's pick is within 0.5 % (geometric mean) of the best measured one, 25 % at most.
+// from HBM: the plan's pick is within 0.7 % (geometric mean) of the best measured one, 23 % at most.
 #define SVDQ_SHAPES(X)                                   \
-  X(442, 4, 4, 2, 4, 2, -6.73, 14.87, 1.333, 0.0, 0.0)   \
-  X(423, 2, 4, 4, 2, 3, -0.81, 6.62, 0.872, 0.0, 0.0)    \
-  X(413, 2, 2, 4, 2, 3, 0.85, 3.58, 0.639, 0.0, 0.0)     \
-  X(224, 2, 2, 2, 4, 4, 0.51, 4.09, 0.525, 0.0, 0.0)     \
-  X(213, 2, 2, 2, 2, 3, 3.03, 0.64, 0.381, 2.16, 0.717)  \
-  X(114, 1, 2, 2, 2, 4, 2.74, 0.86, 0.249, 1.52, 0.490)
+  X(442, 4, 4, 2, 4, 2, -5.64, 13.89, 1.302, 0.0, 0.0)   \
+  X(432, 4, 3, 2, 4, 2, -2.69, 9.82, 1.035, 0.0, 0.0)    \
+  X(423, 2, 4, 4, 2, 3, -0.37, 6.26, 0.863, 0.0, 0.0)    \
+  X(413, 2, 2, 4, 2, 3, 0.83, 3.53, 0.647, 0.0, 0.0)     \
+  X(224, 2, 2, 2, 4, 4, 0.78, 3.91, 0.517, 0.0, 0.0)     \
+  X(213, 2, 2, 2, 2, 3, 3.24, 0.44, 0.381, 2.02, 0.703)  \
+  X(114, 1, 2, 2, 2, 4, 2.52, 1.10, 0.248, 1.79, 0.488)
 struct ShapeInfo {
   int code, tn, tm, waves, wgs;
   double base, fill, step, fill2, step2;
@@ -615,7 +616,7 @@ Plan plan_of(const Fp8Args& a) {
       } else {
         cost += n * (s.fill + S * s.step);
       }
-      if (splits > 1) cost += -0.44 + 0.66 * splits + 0.89 * (s.tn / 64) * (s.tm / 64);  // the partials' round trips
+      if (splits > 1) cost += -0.56 + 0.70 * splits + 0.88 * (s.tn / 64) * (s.tm / 64);  // the partials' round trips
       if (best.shape < 0 || cost < best.cost || (forced > 0 && best.shape == i)) best = Plan{i, (int)tiles, splits, cost};
     }
   }
@@ -646,7 +647,7 @@ Launches launches_of(const Fp8Args& a) {
   const int cus = current_cus();
   const double S = (double)((a.K + 127) / 128);
   double best_cost = best.first.cost;
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 3; ++i) {
     const ShapeInfo& s = kShapes[i];
     const int64_t cols = a.up != nullptr ? s.tn / 2 : s.tn;
     const int64_t nt = (a.N + cols - 1) / cols, mt = (a.M + s.tm - 1) / s.tm;

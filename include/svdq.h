@@ -516,8 +516,9 @@ svdq_status svdq_debug_set_w8a8_plan(int tile, int splits);
  *   defined.
  *   x device bf16 [M, K]; smooth device fp32 [K] or NULL
  *   act_codes device out e4m3 [M, K]; act_scales device out fp32 [KB, M], one row per
- *   block, rows act_scale_stride elements apart (>= M; a run of tokens is a run of each
- *   row, so that a call can write or read part of a larger array; not read where KB = 1)
+ *   block, rows act_scale_stride elements apart (>= M; not read where KB = 1).  A run of
+ *   tokens is a run of each row, from any token on (token scales need 4-byte alignment
+ *   only), so that a call can write or read part of a larger array
  *
  * svdq_fp8_gemm:
  *   Y[m,n] = bf16( epi( sum_b fl32(s_x[b,m] s_w[n/128,b]) (sum_{k in b} q_x[m,k] q_w[n,k]) + bias[n] ) )
@@ -567,7 +568,7 @@ size_t svdq_fp8_gated_gemm_workspace_size(int64_t M, int64_t F, int64_t K, int o
 
 /*
  * Test hook for svdq_fp8_gemm and svdq_fp8_gated_gemm, as svdq_debug_set_w8a8_plan: tile 0
- * chooses by shape, 1 the few-token kernel where M <= 16; 114, 213, 224, 413, 423 and 442 the
+ * chooses by shape, 1 the few-token kernel where M <= 16; 114, 213, 224, 413, 423, 432 and 442 the
  * tile kernel, the digits being the workgroup tile's weight rows / 64 (gated: half of them
  * gate's, half up's), its tokens / 64 and its LDS stages (a tile of fewer than 256 weight
  * rows cannot give coded output, which then takes a tile by shape); splits 0 by shape, else

@@ -21,7 +21,7 @@ GATED = dict(ac=P(1), asc=P(2), ss=5, gc=P(3), gs=P(4), uc=P(5), us=P(6), gb=P(7
 
 @pytest.mark.parametrize("kw,status", [
     (dict(x=None), INVALID_VALUE), (dict(codes=None), INVALID_VALUE), (dict(scales=None), INVALID_VALUE),
-    (dict(x=P(1, 8)), INVALID_VALUE), (dict(smooth=P(2, 4)), INVALID_VALUE), (dict(scales=P(4, 4)), INVALID_VALUE),
+    (dict(x=P(1, 8)), INVALID_VALUE), (dict(smooth=P(2, 4)), INVALID_VALUE), (dict(scales=P(4, 2)), INVALID_VALUE),
     (dict(M=-1), INVALID_VALUE), (dict(K=0), INVALID_VALUE), (dict(K=96), NOT_SUPPORTED), (dict(K=65600), NOT_SUPPORTED),
     (dict(M=(1 << 24) + 1), NOT_SUPPORTED), (dict(ss=4), INVALID_VALUE), (dict(ss=-8), INVALID_VALUE),
     (dict(ss=(1 << 37) + 1), NOT_SUPPORTED),
@@ -48,7 +48,8 @@ def test_gemm_refusals(kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     *[(dict([(n, None)]), INVALID_VALUE) for n in ("ac", "asc", "gc", "gs", "uc", "us", "out", "os")],
-    *[(dict([(n, P(i, 8))]), INVALID_VALUE) for i, n in enumerate(("ac", "asc", "gc", "gs", "uc", "us", "gb", "ub", "smooth", "out", "os"), 1)],
+    *[(dict([(n, P(i, 2 if n in ("asc", "os") else 8))]), INVALID_VALUE)
+      for i, n in enumerate(("ac", "asc", "gc", "gs", "uc", "us", "gb", "ub", "smooth", "out", "os"), 1)],
     (dict(F=96), NOT_SUPPORTED), (dict(K=100), NOT_SUPPORTED), (dict(F=-64), INVALID_VALUE), (dict(F=(1 << 20) + 64), NOT_SUPPORTED),
     (dict(act=2), INVALID_VALUE), (dict(act=-1), INVALID_VALUE), (dict(otype=2), INVALID_VALUE), (dict(otype=0), INVALID_VALUE),
     (dict(ss=0), INVALID_VALUE), (dict(oss=4), INVALID_VALUE), (dict(oss=1 << 38), NOT_SUPPORTED),
@@ -106,7 +107,8 @@ def test_workspace_rules():
 @pytest.mark.skipif(_gpu_visible(), reason="checks the no-GPU path")
 def test_good_calls_reach_the_device_check():
     good = [("svdq_quantize_act_fp8", QUANT, {}), ("svdq_quantize_act_fp8", QUANT, dict(smooth=None, M=1 << 24, K=64, ss=-3)),
-            ("svdq_quantize_act_fp8", QUANT, dict(ss=1000)),
+            ("svdq_quantize_act_fp8", QUANT, dict(ss=1000, scales=P(4, 4))),     # from the second token on
+            ("svdq_fp8_gemm", GEMM, dict(ss=1000, asc=P(2, 12))), ("svdq_fp8_gated_gemm", GATED, dict(ss=100, asc=P(2, 4), oss=100, os=P(11, 8))),
             ("svdq_fp8_gemm", GEMM, {}), ("svdq_fp8_gemm", GEMM, dict(bias=None, ws=None, wsb=0, M=3, epilogue=0)),
             ("svdq_fp8_gemm", GEMM, dict(K=64, ss=0)),                           # one row of scales has no stride
             ("svdq_fp8_gated_gemm", GATED, {}), ("svdq_fp8_gated_gemm", GATED, dict(otype=0, smooth=None, os=None, oss=0, ws=None, wsb=0)),

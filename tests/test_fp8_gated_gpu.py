@@ -83,7 +83,7 @@ def test_gated_codes(M, N, K, smooth):
     _check_out(got, *c, "silu", sm)
 
 
-@pytest.mark.parametrize("tile", [1, 114, 213, 224, 413, 423, 442])
+@pytest.mark.parametrize("tile", [1, 114, 213, 224, 413, 423, 432, 442])
 @pytest.mark.parametrize("splits", [1, 2, 16])
 @pytest.mark.parametrize("quantize", [None, "fp8"])
 def test_every_tile_and_split(tile, splits, quantize):
@@ -98,6 +98,33 @@ def test_every_tile_and_split(tile, splits, quantize):
         finally:
             P.debug_set_fp8_plan()
         _check_out(got, *c, "silu")
+
+
+@pytest.mark.parametrize("M,N,K", [(2304, 4608, 192), (2560, 4096, 512), (3840, 4096, 256), (2570, 4160, 256), (4100, 6144, 192), (2050, 8192, 448)])
+@pytest.mark.parametrize("quantize", [None, "fp8"])
+def test_whole_rounds_and_the_rest(M, N, K, quantize):
+    """As for the plain product, bf16 against a small tile, codes against the smallest that
+    holds a block of features; codes of some tokens against the oracle."""
+    import torch
+    import bit_diffusion_transformer_svdq_amd as P
+    c = _case(M, N, K, 8)
+
+    def bits():
+        r = _call(*c, quantize=quantize)
+        return [t.view(torch.uint8) for t in (r if isinstance(r, tuple) else (r,))], r
+    got, out = bits()
+    for tile in (413 if quantize else 114, 432, 442):
+        P.debug_set_fp8_plan(tile, 1)
+        try:
+            want, _ = bits()
+        finally:
+            P.debug_set_fp8_plan()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), tile
+    rows = np.unique(np.concatenate([np.arange(0, M, 97), [M - 1]]))
+    part = (c[0][0][rows], c[0][1][:, rows]), *c[1:]
+    at = torch.from_numpy(rows).cuda()
+    some = out[at] if quantize is None else (out[0].view(torch.uint8)[at].view(torch.float8_e4m3fn), out[1][:, at])
+    _check_out(some, *part, "silu")
 
 
 @pytest.mark.parametrize("M", [3, 16, 70, 300])

@@ -111,7 +111,7 @@ def test_gemm(M, N, K, epilogue):
     _check_gemm(host(y), x, w, b, epilogue)
 
 
-@pytest.mark.parametrize("tile", [1, 114, 213, 224, 413, 423, 442])
+@pytest.mark.parametrize("tile", [1, 114, 213, 224, 413, 423, 432, 442])
 @pytest.mark.parametrize("splits", [1, 2, 16])
 def test_every_tile_and_split(tile, splits):
     """The same shapes on every kernel, tile and split: one stage and less, odd numbers of
@@ -197,7 +197,7 @@ def test_runs_of_tokens():
     K, N = 448, 192
     w = weights(N, K, 5)
     wd = dev_codes(w[0]), dev(w[1])
-    for a, b in ((4, 9), (8, 140)):
+    for a, b in ((4, 9), (8, 140), (1, 2), (3, 19), (7, 151)):
         x, _ = acts(200, K, 5)
         codes = torch.full((200, K), 7, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
         scales = torch.full((4, 200), 7.0, device="cuda")
@@ -227,6 +227,29 @@ def test_codes_far_into_memory():
     assert not bool(y[:-100].any())
     y = P.fp8_gemm(codes[-100:], wide[:, -100:], dev_codes(w[0]), dev(w[1]))
     _check_gemm(host(y), x, w, None, "none")
+
+
+@pytest.mark.parametrize("M,N,K", [(2304, 9216, 448), (2560, 8192, 256), (4608, 6144, 512), (2570, 8192, 256), (4160, 12288, 192),
+                                   (2050, 16384, 512), (33000, 640, 128), (3840, 12288, 320)])
+def test_whole_rounds_and_the_rest(M, N, K):
+    """Products of more than one round of the largest tiles run as workgroups that stay for
+    several tiles, or as two launches: every row is that of one launch of a small tile, bit
+    for bit (blocks are added in the order of K on every tile)."""
+    import torch
+    import bit_diffusion_transformer_svdq_amd as P
+    d = _dev(tokens(M, K, 8), weights(N, K, 8))
+    b = torch.randn(N, device="cuda").bfloat16()
+    y = P.fp8_gemm(*d, b)
+    P.debug_set_fp8_plan(114, 1)
+    try:
+        one = P.fp8_gemm(*d, b)
+        P.debug_set_fp8_plan(442, 1)
+        big = P.fp8_gemm(*d, b)
+        P.debug_set_fp8_plan(432, 1)
+        mid = P.fp8_gemm(*d, b)
+    finally:
+        P.debug_set_fp8_plan()
+    assert torch.equal(y, one) and torch.equal(big, one) and torch.equal(mid, one)
 
 
 def test_packed_linear():

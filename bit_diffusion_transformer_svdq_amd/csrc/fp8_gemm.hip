@@ -47,6 +47,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <array>
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -662,10 +663,9 @@ Fp8Args part_of(const Fp8Args& a, int64_t m0, int64_t m1) {
   if (a.out_scales != nullptr) part.out_scales += m0;
   return part;
 }
-Launches launches_of(const Fp8Args& a) {
+Launches plan_launches(const Fp8Args& a, bool forced, int cus) {
   Launches best{a.M, plan_of(a), Plan{}};
-  if (g_tile.load(std::memory_order_relaxed) > 1 || g_splits.load(std::memory_order_relaxed) > 0) return best;
-  const int cus = current_cus();
+  if (forced) return best;
   const double S = (double)((a.K + 127) / 128);
   double best_cost = best.first.cost;
   for (int i = 0; i < 3; ++i) {
@@ -684,6 +684,21 @@ Launches launches_of(const Fp8Args& a) {
     }
   }
   return best;
+}
+
+// Planned once for a call's workspace query, its check and its launch: a thread keeps its
+// last plan, by all that it depends on (up to 1 us each time otherwise).
+Launches launches_of(const Fp8Args& a) {
+  struct Last {
+    std::array<int, 7> key;
+    Launches plan;
+  };
+  thread_local Last last{};
+  const int tile = g_tile.load(std::memory_order_relaxed), splits = g_splits.load(std::memory_order_relaxed);
+  const int cus = current_cus();
+  const std::array<int, 7> key{a.M, a.N, a.K, (int)form_of(a), tile, splits, cus};
+  if (last.key != key) last = Last{key, plan_launches(a, tile > 1 || splits > 0, cus)};
+  return last.plan;
 }
 
 template <int H, int J, int WN, int WM, int R, Form kForm>

@@ -37,11 +37,12 @@
 //    not depend on timing;
 //  * many tiles: a workgroup stays and takes one after the other, as in w8a8_gemm.hip.
 //
-// 8192^3 takes 2.5 PFLOP/s and 4096 x 8192 -> 4096 113.7 us, 2.4; with all codes zero 89.5 us: on
-// random codes large products are bound by the chip's power (the clock falls from 2.3 to 2.0
-// GHz), otherwise by the MFMAs and fmas (74 us without the stages' loads, LDS reads and
-// barriers).  A round of 256 x 256 tiles on all compute units takes 1.65 us per stage and 6 to 7
-// us for its Y, which all of them write at once.
+// 8192^3 takes 2.5-2.7 PFLOP/s and 4096 x 8192 -> 4096 109-114 us, 2.4-2.5; with all codes zero 81 us:
+// on random codes large products are bound by the chip's power (the clock falls from 2.3
+// to 2.0 GHz), otherwise by the MFMAs and fmas.  The second one without the stages' loads 94 us
+// (zero codes 74), without the LDS reads 101 (78), without both 88 (71): what is left are the MFMAs,
+// fmas, barriers and Y.  A round of 256 x 256 tiles on all compute units takes 1.65 us per stage
+// and 6 to 7 us for its Y, which all of them write at once.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

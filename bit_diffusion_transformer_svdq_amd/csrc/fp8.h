@@ -9,9 +9,10 @@ namespace svdq {
 
 constexpr int kFp8Block = 128;
 
-// SiLU, x / (1 + exp(-x)): relative error below (|x| + 5) 2^-24 for x > -87 (the
-// product with log2(e) is rounded); beyond, where the reciprocal is subnormal and
-// v_rcp_f32 gives zero, values below 1e-36 in magnitude come out as -0
+// SiLU, x / (1 + exp(-x)): relative error below (1.23 |x| + 6) 2^-24 for x > -87 (the
+// product with log2(e) is rounded, |x| of it, and log2(e) itself is off by 0.23 2^-24);
+// beyond, where the reciprocal is subnormal and v_rcp_f32 gives zero, values below
+// 1e-36 in magnitude come out as -0
 __device__ __forceinline__ float silu_exp2(float x) {
   return x * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(-1.442695041f * x) + 1.0f);
 }

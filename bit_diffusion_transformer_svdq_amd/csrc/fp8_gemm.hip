@@ -753,18 +753,34 @@ hipError_t tile_go(const TileArgs& t, int tiles, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The weight-streaming kernel for up to 16 tokens, but for long K (up to 4 tokens, and
-// gated not at all) and many rows (up to 4 tokens); always into codes.  Measured, it against
-// the best tile, weights from HBM, us, 1 / 16 tokens: 3072 -> 3072 4.2 / 5.2 against 7.9 / 8.1;
-// 3072 -> 12288 10.2 / 12.9 against 12.7 / 13.0; 12288 -> 3072 13.1 / 16.1 against 13.6 / 13.8; gated 3072 ->
-// 3072 6.6 / 8.0 against 8.8 / 9.0, 2304 -> 6144 8.6 / 10.4 against 9.0 / 9.0, 8192 -> 1024 11.6 / 14.6
-// against 10.2 / 10.3; into codes 3072 -> 3072 8.6 / 10.0 against 14.1 / 14.4.
+// The weight-streaming kernel for up to 16 tokens, but where K is long beside its N / 16
+// workgroups, which do not divide K among themselves, or the rows are many.  Measured, it
+// against the best tile and split, weights from HBM, us, 1 / 4 / 16 tokens
+// (profiles/few_token_rule_fp8.txt):
+//   plain  4096 -> 2048      5.3 / 5.6 / 6.4*     against  8.2 / 8.3 / 8.2
+//          4096 -> 16384    14.9 / 15.4* / 20.2            17.4 / 17.4 / 17.4*
+//          8192 -> 64        6.4 / 7.0* / 9.0              7.5 / 7.5 / 7.5*
+//         16384 -> 64       10.6 / 12.1 / 16.1             8.8 / 8.7 / 8.7*
+//         16384 -> 4096     16.1 / 16.8* / 21.1            18.4 / 18.5 / 19.0*
+//         65536 -> 64       37.0 / 42.4 / 57.9             14.1 / 14.1 / 14.0*
+//   gated  4096 -> 2048      7.8 / 8.0 / 8.9*              9.3 / 9.4 / 9.4
+//          8192 -> 1024     11.7 / 12.4 / 14.6             10.0 / 10.0 / 10.1*
+//          8192 -> 4096     16.1 / 16.5* / 18.5            17.4 / 17.4 / 17.5*
+//         16384 -> 8192     49.6 / 49.5* / 56.4            58.0 / 58.0 / 58.5*
+//         65536 -> 64       66.9 / 72.6 / 90.5             15.0 / 15.0 / 15.1*
+//   codes  8192 -> 64       11.1 / 11.8 / 13.9*            14.5 / 14.5 / 14.5
+//         16384 -> 64       18.9 / 20.3* / 24.4            17.7 / 17.7 / 17.7*
+//         16384 -> 1024     21.0 / 22.2* / 26.7            22.7 / 22.9 / 23.3*
+//         65536 -> 64       66.8 / 72.0 / 89.1             31.4 / 31.4 / 31.6*
+// (* marks the side the rule takes, up to 4 and up to 16 tokens.)
 bool few_tokens(const Fp8Args& a) {
   const int t = g_tile.load(std::memory_order_relaxed);
   if (t > 1 || a.M > 16) return false;
-  if (t == 1 || a.out_scales != nullptr) return true;
+  if (t == 1) return true;
   const bool gated = a.up != nullptr;
-  if (a.K > 4096) return !gated && a.M <= 4;
+  if (a.out_scales != nullptr) return a.K <= (a.M <= 4 ? 16384 : 8192);
+  if (a.K > (gated ? 4096 : 8192)) return a.M <= 4 && a.N >= 4096;  // a workgroup for each compute unit
+  if (a.K > 4096) return a.M <= 4;
   return a.M <= 4 || (gated ? 2 : 1) * (int64_t)a.N <= 8192;
 }
 

@@ -757,21 +757,21 @@ hipError_t tile_go(const TileArgs& t, int tiles, hipStream_t stream) {
 // workgroups, which do not divide K among themselves, or the rows are many.  Measured, it
 // against the best tile and split, weights from HBM, us, 1 / 4 / 16 tokens
 // (profiles/few_token_rule_fp8.txt):
-//   plain  4096 -> 2048      5.3 / 5.6 / 6.4*     against  8.2 / 8.3 / 8.2
-//          4096 -> 16384    14.9 / 15.4* / 20.2            17.4 / 17.4 / 17.4*
-//          8192 -> 64        6.4 / 7.0* / 9.0              7.5 / 7.5 / 7.5*
-//         16384 -> 64       10.6 / 12.1 / 16.1             8.8 / 8.7 / 8.7*
-//         16384 -> 4096     16.1 / 16.8* / 21.1            18.4 / 18.5 / 19.0*
-//         65536 -> 64       37.0 / 42.4 / 57.9             14.1 / 14.1 / 14.0*
-//   gated  4096 -> 2048      7.8 / 8.0 / 8.9*              9.3 / 9.4 / 9.4
-//          8192 -> 1024     11.7 / 12.4 / 14.6             10.0 / 10.0 / 10.1*
-//          8192 -> 4096     16.1 / 16.5* / 18.5            17.4 / 17.4 / 17.5*
-//         16384 -> 8192     49.6 / 49.5* / 56.4            58.0 / 58.0 / 58.5*
-//         65536 -> 64       66.9 / 72.6 / 90.5             15.0 / 15.0 / 15.1*
-//   codes  8192 -> 64       11.1 / 11.8 / 13.9*            14.5 / 14.5 / 14.5
-//         16384 -> 64       18.9 / 20.3* / 24.4            17.7 / 17.7 / 17.7*
-//         16384 -> 1024     21.0 / 22.2* / 26.7            22.7 / 22.9 / 23.3*
-//         65536 -> 64       66.8 / 72.0 / 89.1             31.4 / 31.4 / 31.6*
+//   plain  4096 -> 2048   5.2 / 5.6* / 6.4*       against  8.2 / 8.3 / 8.3
+//          4096 -> 16384  14.9 / 15.4* / 20.3     against  17.4 / 17.5 / 17.5*
+//          8192 -> 64     6.4 / 7.0* / 9.0        against  7.5 / 7.5 / 7.5*
+//         16384 -> 64     10.7 / 12.0 / 16.0      against  8.8 / 8.7* / 8.8*
+//         16384 -> 4096   15.9 / 16.6* / 21.3     against  18.6 / 18.8 / 19.2*
+//         65536 -> 64     36.9 / 42.4 / 57.9      against  14.2 / 14.0* / 14.0*
+//   gated  4096 -> 2048   7.8 / 7.9* / 8.9*       against  9.3 / 9.4 / 9.4
+//          8192 -> 1024   11.6 / 12.4 / 14.6      against  9.9 / 9.9* / 10.1*
+//          8192 -> 4096   16.2 / 16.6* / 18.4     against  17.4 / 17.9 / 17.9*
+//         16384 -> 8192   49.1 / 49.7* / 56.9     against  46.7 / 50.8 / 51.3*
+//         65536 -> 64     67.1 / 72.6 / 90.6      against  14.8 / 14.8* / 14.9*
+//   codes  8192 -> 64     11.2 / 11.7* / 14.0*    against  14.4 / 14.4 / 14.5
+//         16384 -> 64     19.0 / 20.2* / 24.3     against  17.6 / 17.7 / 17.8*
+//         16384 -> 1024   21.0 / 22.2* / 26.7     against  22.8 / 22.9 / 23.3*
+//         65536 -> 64     66.3 / 72.2 / 89.2      against  31.4 / 31.5* / 31.6*
 // (* marks the side the rule takes, up to 4 and up to 16 tokens.)
 bool few_tokens(const Fp8Args& a) {
   const int t = g_tile.load(std::memory_order_relaxed);

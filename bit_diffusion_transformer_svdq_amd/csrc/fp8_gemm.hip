@@ -596,9 +596,14 @@ struct Plan {
 // Workgroup tiles, the test hook's name of each (weight rows / 64, tokens / 64, LDS stages)
 // and what a launch takes by the model of w8a8_gemm.hip: base + n (fill + S step) us with n
 // workgroups on the busiest compute unit and S stages of 128 k, pairs of workgroups at fill2
-// and step2 where two share a compute unit.  Fitted to 554 shapes (17 to 4608 tokens, K 512
-// to 10240, 384 to 12288 rows, 40 % of them gated), every tile and split timed with weights
-// from HBM: the plan's pick is within 0.7 % (geometric mean) of the best measured one, 23 % at most.
+// and step2 where two share a compute unit.  Fitted to picks, not to times: to 554 shapes (17
+// to 4608 tokens, K 512 to 10240, 384 to 12288 rows, 40 % of them gated), times far from a
+// shape's best weighing less.  On 2373 other shapes (profiles/plan_sweep_fp8.txt) what a
+// call takes is 0.2 % from the best tile and split on the geometric mean, 29 % at most (817 x 9344 ->
+// 2816: 432 in 4 splits 51.6 us, 224 whole 40.0).  The times that it gives are 7 % low on the mean,
+// 13 % (up to 23) for 4096 and more tokens with K from 8192, where power lowers the clock:
+// a round of 442 takes 1.65 us a stage there, not 1.302.  Its picks are as near the best there: 2.7 %
+// below the best single launch on the mean, 26 % above at most (4150 x 15360 -> 576: 442 in 4 splits 73.5 us, 224 whole 58.2).
 #define SVDQ_SHAPES(X)                                   \
   X(442, 4, 4, 2, 4, 2, -5.64, 13.89, 1.302, 0.0, 0.0)   \
   X(432, 4, 3, 2, 4, 2, -2.69, 9.82, 1.035, 0.0, 0.0)    \

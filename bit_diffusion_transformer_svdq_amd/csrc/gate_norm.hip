@@ -417,7 +417,7 @@ int waves_for(int64_t M, int c8, int per_lane) {
 //             smoothed, 2048 x 6144: W4V3 10.8*, W8V2 11.5;  1024 x 4608: W4V3 7.0*, W8V2 7.9;
 //             512 x 3072: W2V3 4.8, W4V2 4.4*
 //  The norm with 8-bit output and reciprocals: 4608 x 3072 W2V3 27.3, W4V2 24.1*, W8V1 29.5.
-//  Codes with a scale per 128 channels take what int8 codes do and 0.5 to 1 us for the scales, which leave
+//  Codes with a scale per 128 channels take what int8 codes do and 0.7 to 1.3 us for the scales, which leave
 //  one by one (4608 x 3072 24.6 against 23.9 us, with reciprocals 28.7 against 27.4).
 constexpr int kNormPerLane = 3, kNormInt8PerLane = 2, kQuantPerLane = 8, kQuantSmoothPerLane = 3;
 

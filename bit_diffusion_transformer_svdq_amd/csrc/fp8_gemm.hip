@@ -135,7 +135,9 @@ __global__ __launch_bounds__((Shape<H, J, WN, WM, R>::kThreads), 2) void fp8_til
   typedef const float __attribute__((address_space(4))) cfloat;
   cfloat *ws0, *ws1;
   float sw0, sw1;
-  // the half stage sums its 64 products twice (below)
+  // the half stage sums its 64 products twice (below) and halves the weights' scale, which
+  // is exact but for odd multiples of 2^-149 below 2^-125.  (Halving s_x s_w is always exact
+  // and took 1 % of the large products, zeros in the tokens' registers made the largest tile spill.)
   const int half_at = q_end == S_all && (K & 64) != 0 ? S - 1 : S;
   auto load_ws = [&](int q) {
     const int at = min(q, S - 1);

@@ -544,6 +544,10 @@ svdq_status svdq_debug_set_w8a8_plan(int tile, int splits);
  *   scales fp32 [ceil(F / 128), M] (rows out_scale_stride apart) that svdq_fp8_gemm reads:
  *   those of svdq_quantize_act_fp8 for v = fl32(H fl32(1/smooth)) (smooth fp32 [F]), or H,
  *   in fp32 in the place of x_hat, not rounded to bf16 in between.
+ *   (What the matrix cores cut off G and U, above, is 4e-5 of a block's largest H, root mean
+ *   square, on normal activations with outliers: 0.35 % of the codes are the neighbours of those that exact
+ *   sums give, with fp32 products 0.007 %, and Y of a whole block is 2.1e-3 to 2.6e-3 from the 64-bit value,
+ *   relative, root mean square, with fp32 products 1.7e-3.)
  *   workspace of svdq_fp8_gated_gemm_workspace_size(M, F, K, out_type) bytes
  * K, N, F % 64 == 0, M <= 2^24, N, F <= 2^20, K <= 65536, strides <= 2^37 (NOT_SUPPORTED
  * beyond); M == 0 is a no-op; INVALID_VALUE for an unknown enum value, smooth without

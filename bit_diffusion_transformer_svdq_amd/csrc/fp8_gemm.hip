@@ -5,9 +5,10 @@
 //
 // A block is exactly the K of one v_mfma_f32_16x16x128_f8f6f4 (32 cycles, 2048 operations
 // a cycle and SIMD): every MFMA starts from zero and its four results per lane join the
-// fp32 sums by one fma each with the block's scale.  (From registers, two waves per SIMD, an
-// MFMA with 4 such fmas takes 33.7 cycles, with 6 38: the vector unit works beside the
-// matrix core, with little to spare for anything but the fmas.)  With the weights as the A
+// fp32 sums by one fma each with the block's scale.  (From registers, two waves per SIMD, on
+// zero codes, an MFMA with its 4 fmas takes 1.11 times as long as one alone, 35.4 cycles
+// (profiles/rates_fp8_operators.txt): the vector unit works beside the matrix core, with
+// little to spare for anything but the fmas.)  With the weights as the A
 // operand a lane's results belong to one token, so the scale s_x s_w is one product per
 // token tile and block, not one per result.
 //
@@ -38,7 +39,7 @@
 //    not depend on timing;
 //  * many tiles: a workgroup stays and takes one after the other, as in w8a8_gemm.hip.
 //
-// 8192^3 takes 2.5-2.7 PFLOP/s and 4096 x 8192 -> 4096 109-114 us, 2.4-2.5; with all codes zero 81 us:
+// 8192^3 takes 2.5 PFLOP/s and 4096 x 8192 -> 4096 108-113 us, 2.4-2.5; with all codes zero 80 us:
 // on random codes large products are bound by the chip's power (the clock falls from 2.3
 // to 2.0 GHz), otherwise by the MFMAs and fmas.  The second one without the stages' loads 94 us
 // (zero codes 74), without the LDS reads 101 (78), without both 88 (71): what is left are the MFMAs,
